@@ -7,7 +7,9 @@ PyTorch supplies device memory and streams. There is no fallback: if the
 library cannot be loaded, importing this package raises.
 
 The functions below carry the C names; ``Table`` wraps them for torch
-tensors.
+tensors. ``ops`` (whose names are found here too) holds the dense operators:
+an uncompressed table's lookup and gradient, the norm of looked-up rows, and
+their 8-bit quantiser and product.
 """
 from __future__ import annotations
 
@@ -588,3 +590,10 @@ class MixedTable(Table):
         if st != CP_OK:
             raise CPError(st, "cp_table_download")
         return out
+
+
+# the dense operators: ops.py builds on the names above
+from . import ops as _ops  # noqa: E402
+from .ops import *  # noqa: E402,F401,F403
+
+__all__ += _ops.__all__

@@ -1,5 +1,5 @@
 """Builds the HIP libraries for gfx950 with hipcc, in-tree: libcp.so (the
-lookup library, include/cp.h) and libcp_probe.so (measurement probes,
+lookup library, include/cp.h and include/cp_ops.h) and libcp_probe.so (measurement probes,
 include/cp_probe.h)."""
 from __future__ import annotations
 
@@ -13,10 +13,13 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "cp_decode.hip"), os.path.join(CSRC, "cp_dedup.hip"),
            os.path.join(CSRC, "cp_encode.hip"), os.path.join(CSRC, "cp_mixed.hip"),
            os.path.join(CSRC, "cp_shard.hip"), os.path.join(CSRC, "cp_dedup_mixed.hip"),
-           os.path.join(CSRC, "cp_api.hip")]
+           os.path.join(CSRC, "cp_api.hip"),
+           os.path.join(CSRC, "cp_embed.hip"), os.path.join(CSRC, "cp_norm.hip"), os.path.join(CSRC, "cp_quant.hip"),
+           os.path.join(CSRC, "cp_gemm.hip"), os.path.join(CSRC, "cp_ops_api.hip")]
 DEPS = SOURCES + [os.path.join(CSRC, "cp_internal.h"), os.path.join(CSRC, "cp_lane.h"),
                   os.path.join(CSRC, "cp_encode_copies.h"),
-                  os.path.join(ROOT, "include", "cp.h")]
+                  os.path.join(CSRC, "cp_status.h"), os.path.join(CSRC, "cp_ops_internal.h"),
+                  os.path.join(ROOT, "include", "cp.h"), os.path.join(ROOT, "include", "cp_ops.h")]
 LIB = os.path.join(PKG, "libcp.so")
 PROBE_SOURCES = [os.path.join(CSRC, "cp_probe.hip")]
 PROBE_LIB = os.path.join(PKG, "libcp_probe.so")

@@ -8,6 +8,7 @@
 
 #include "../../include/cp.h"
 #include "cp_internal.h"
+#include "cp_status.h"
 
 struct cp_table {
     cp_table_desc desc;     // bits_per_step = 0 for a mixed-rate table
@@ -45,6 +46,8 @@ static cp_status hip_fail(hipError_t e)
     return (e == hipErrorOutOfMemory || e == hipErrorMemoryAllocation) ? CP_ERR_OUT_OF_MEMORY
                                                                          : CP_ERR_HIP;
 }
+
+cp_status cpk::status_of(hipError_t e) { return e == hipSuccess ? CP_OK : hip_fail(e); }
 
 // Makes the table's device current for the duration of a call and restores
 // the caller's device afterwards (launches on the null stream, copies and

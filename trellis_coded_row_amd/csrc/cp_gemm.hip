@@ -1,0 +1,576 @@
+// cp_gemm.hip - out[m][n] = sum over k of A[m][k] B[n][k] for e4m3 operands
+// with an e8m0 scale for each 128 values of k.
+//
+// 16-bit outputs use the scaled matrix instruction of gfx950 (16 x 16 outputs,
+// 128 values of k): lane l carries row l % 16 and 32 of its 128 values, and
+// every lane of a row is given that row's e8m0 scale for the group, so the
+// scales cost no arithmetic. Which 32 values a lane carries does not matter
+// as long as both operands agree: here 16 from the group's first half and 16
+// from the second. That instruction adds its products in groups of 8, each
+// cut off 16 bits below its largest (measured: 1.5e-5 of the result's rms at
+// any k), which is far below a 16-bit output's rounding.
+//
+// 32-bit outputs are not to lose that, so there each value times its scale
+// is converted to bf16 (e4m3 has 4 significant bits: exact) on the way from
+// LDS to the bf16 matrix instruction (measured: 1e-8 to 2e-7 of the result's
+// rms, the 32-bit sum's own rounding), at half the rate.
+//
+// The operands are passed swapped (B's rows as the instruction's rows), so
+// that a lane's four results are neighbours in an output row.
+#include <type_traits>
+
+#include "cp_ops_internal.h"
+
+namespace cpk {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr uint32_t kStep = 128;              // values of k per step (one scale group)
+constexpr uint32_t kOutside = 0x80000000u;   // a buffer offset past any tile: loads give zeros
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, 0x7FFFFFFF, 0x00020000);
+}
+
+// The scales are byte S of sb and sa.
+template <int S>
+__device__ __forceinline__ f32x4 mfma(i32x8 b, i32x8 a, f32x4 c, int sb, int sa)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 0, 0, S, sb, S, sa);
+}
+
+__device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi)
+{
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// The float whose exponent is scale byte S of a dword (what the conversion
+// reads of its scale).
+template <int S>
+__device__ __forceinline__ float scale_of(int scales)
+{
+    return __int_as_float(((scales >> (8 * S)) & 0xFF) << 23);
+}
+
+// 32 scaled e4m3 values in bf16.
+struct Wide {
+    bf16x8 v[4];
+};
+
+__device__ __forceinline__ Wide widen(i32x8 x, float scale)
+{
+    Wide w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q], scale, false);
+        const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q], scale, true);
+        const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q + 1], scale, false);
+        const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * q + 1], scale, true);
+        w.v[q] = bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+    }
+    return w;
+}
+
+__device__ __forceinline__ f32x4 mfma_wide(const Wide &b, const Wide &a, f32x4 c)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[q], a.v[q], c, 0, 0, 0);
+    return c;
+}
+
+// 8 neighbouring outputs of a row of n.
+__device__ __forceinline__ void put_out(void *out, int dtype, uint64_t row, uint64_t stride, uint32_t c, uint32_t n,
+                                        const float *f)
+{
+    if (c >= n) return;
+    if (dtype == kBF16) store8<kBF16>((uint16_t *)out + row * stride, c, n, f);
+    else if (dtype == kF16) store8<kF16>((uint16_t *)out + row * stride, c, n, f);
+    else store8<kF32>((float *)out + row * stride, c, n, f);
+}
+
+struct TileParams {
+    const uint8_t *a, *a_scale, *b, *b_scale;
+    uint32_t a_stride, a_scale_stride, b_stride, b_scale_stride;
+    uint32_t m, n, k;
+    uint32_t tiles_m, tiles_n, steps_per_split;
+    void *out;
+    uint64_t out_stride, split_stride;  // split_stride: elements between the splits' outputs
+    int out_dtype;
+};
+
+// Tiles of 32 FM x 32 FN outputs; four waves, 2 x 2, each with FM x FN
+// fragments of 16 x 16. A step's operands (128 values of k) are copied to
+// LDS by loads that bypass the registers, one step ahead, into the other of
+// two buffers. One barrier per step, before the last pair of A fragments is
+// multiplied: by then every wave has read all it needs of this step and its
+// own copies of the next have landed, so the first fragments of the next
+// step are read, and the copies of the step after it start, under those
+// products.
+//
+// LDS: a row's 128 bytes are 8 chunks of 16; chunk c of the fragment row r
+// stands at c ^ (r / 2). A 16-byte LDS read serves 16 lanes at a time, 8 of
+// them with odd rows and 8 with even ones (which lie 128 bytes apart, in
+// different halves of the banks); the exchange spreads each 8 over the 8
+// chunks of a row. The copy to LDS writes lane after lane, so the exchange
+// is made in the address that a lane loads from, inside one 128-byte line.
+//
+// B's fragment f has rows n = 4 FB (r / 4) + 4 f + r % 4 of a block of 16 FB
+// (FB = up to 4 fragments): a lane's results from the FB fragments are then
+// 4 FB neighbours in its output row.
+template <int FM, int FN, bool BLOCKS, bool KTAIL, bool EXACT>
+__global__ __launch_bounds__(256) void gemm_tile(TileParams p)
+{
+    constexpr uint32_t BM = 32 * FM, BN = 32 * FN;
+    constexpr int FB = FN < 4 ? FN : 4, NG = FM / 2;
+    constexpr int LA = BM / 32, LB = BN / 32;  // copies of 8 rows per wave
+    __shared__ __attribute__((aligned(16))) uint8_t as0[BM * kStep], as1[BM * kStep], bs0[BN * kStep],
+        bs1[BN * kStep];
+    const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t wm = w >> 1, wn = w & 1u, r = lane & 15u, g = lane >> 4;
+    // workgroup id -> tile: each of the 8 XCDs (ids taken in turn) gets a
+    // contiguous run of tiles, which go down 8 tile rows at a time, so that
+    // the operands an XCD reads at one time are few enough for its own L2
+    const uint32_t ntiles = p.tiles_m * p.tiles_n, total = gridDim.x;
+    const uint32_t xcd = blockIdx.x & 7u, per = total >> 3, extra = total & 7u;
+    const uint32_t id = xcd * per + (xcd < extra ? xcd : extra) + (blockIdx.x >> 3);
+    const uint32_t split = id / ntiles, tile = id % ntiles;
+    const uint32_t band = tile / (8 * p.tiles_n), band_m = band * 8;
+    const uint32_t band_rows = p.tiles_m - band_m < 8 ? p.tiles_m - band_m : 8;
+    const uint32_t in_band = tile - band * 8 * p.tiles_n;
+    const uint32_t m0 = (band_m + in_band % band_rows) * BM, n0 = (in_band / band_rows) * BN;
+    const uint32_t all_steps = (p.k + kStep - 1) / kStep;
+    const uint32_t s0 = split * p.steps_per_split;
+    const uint32_t s1 = s0 + p.steps_per_split < all_steps ? s0 + p.steps_per_split : all_steps;
+    const uint32_t steps = s1 - s0;
+
+    const auto ra = buffer_of(p.a + (uint64_t)m0 * p.a_stride), rb = buffer_of(p.b + (uint64_t)n0 * p.b_stride);
+    // where this lane's part of each copy comes from (rows past the end: the last one)
+    uint32_t va[LA], vb[LB], ca[LA], cb[LB];
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const uint32_t row = (w * LA + i) * 8 + (lane >> 3), in = m0 + row < p.m ? row : p.m - 1 - m0;
+        ca[i] = ((lane & 7u) ^ ((row >> 1) & 7u)) * 16;
+        va[i] = in * p.a_stride + ca[i];
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+        const uint32_t row = (w * LB + i) * 8 + (lane >> 3), in = n0 + row < p.n ? row : p.n - 1 - n0;
+        cb[i] = ((lane & 7u) ^ (((row / (4 * FB)) & 3u) << 1 | ((row >> 1) & 1u))) * 16;
+        vb[i] = in * p.b_stride + cb[i];
+    }
+    const auto copy = [&](uint32_t s, uint8_t *as, uint8_t *bs) {
+        const uint32_t k0 = (s < s1 ? s : s1 - 1) * kStep;  // past the end: the last step again, never read
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            const uint32_t v = KTAIL && k0 + ca[i] >= p.k ? kOutside : va[i];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(as + (w * LA + i) * 1024), 16, v, k0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < LB; ++i) {
+            const uint32_t v = KTAIL && k0 + cb[i] >= p.k ? kOutside : vb[i];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(bs + (w * LB + i) * 1024), 16, v, k0, 0, 0);
+        }
+    };
+    // k ends inside a chunk: its bytes past k, which may hold anything, are
+    // cleared in LDS
+    const auto clear_tail = [&](uint8_t *as, uint8_t *bs) {
+        const uint32_t chunk = (p.k % kStep) / 16, keep = p.k % 16;
+        for (uint32_t row = threadIdx.x; row < BM + BN; row += 256) {
+            uint8_t *at;
+            if (row < BM) at = as + row * kStep + (chunk ^ ((row >> 1) & 7u)) * 16;
+            else {
+                const uint32_t rw = row - BM;
+                at = bs + rw * kStep + (chunk ^ (((rw / (4 * FB)) & 3u) << 1 | ((rw >> 1) & 1u))) * 16;
+            }
+            for (uint32_t e = keep; e < 16; ++e) at[e] = 0;
+        }
+        __syncthreads();
+    };
+    const bool partial_chunk = KTAIL && p.k % 16 != 0 && s1 == all_steps;
+
+    const uint32_t oa = (wm * FM * 16 + r) * kStep + (g ^ (r >> 1)) * 16;
+    const uint32_t ob = (wn * FN * 16 + (r >> 2) * (4 * FB) + (r & 3u)) * kStep + (g ^ (r >> 1)) * 16;
+    const auto read_a = [&](const uint8_t *as, int i) {
+        return join(*reinterpret_cast<const i32x4 *>(as + oa + i * 16 * kStep),
+                    *reinterpret_cast<const i32x4 *>(as + (oa ^ 64u) + i * 16 * kStep));
+    };
+    const auto read_b = [&](const uint8_t *bs, int f) {
+        const uint32_t at = (f / FB) * 16 * FB * kStep + (f % FB) * 4 * kStep;
+        return join(*reinterpret_cast<const i32x4 *>(bs + ob + at),
+                    *reinterpret_cast<const i32x4 *>(bs + (ob ^ 64u) + at));
+    };
+    // scales: a dword has a row's bytes for four steps; one row of scales for
+    // a wave's columns where they are for blocks
+    constexpr int NB = BLOCKS ? 1 : FN;
+    const uint8_t *psa[FM], *psb[NB];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const uint32_t row = m0 + wm * FM * 16 + i * 16 + r;
+        psa[i] = p.a_scale + (uint64_t)(row < p.m ? row : p.m - 1) * p.a_scale_stride;
+    }
+#pragma unroll
+    for (int f = 0; f < NB; ++f) {
+        const uint32_t c0 = n0 + wn * FN * 16;
+        uint32_t row = BLOCKS ? c0 : c0 + (f / FB) * 16 * FB + (r >> 2) * (4 * FB) + (f % FB) * 4 + (r & 3u);
+        row = row < p.n ? row : p.n - 1;
+        psb[f] = p.b_scale + (uint64_t)(BLOCKS ? row / 128 : row) * p.b_scale_stride;
+    }
+    int sa[FM], sb[NB], na[FM], nb[NB];
+    const auto load_scales = [&](uint32_t s, int *ta, int *tb) {
+        const uint32_t at = (s < s1 ? s : s1 - 1) & ~3u;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) ta[i] = *reinterpret_cast<const int *>(psa[i] + at);
+#pragma unroll
+        for (int f = 0; f < NB; ++f) tb[f] = *reinterpret_cast<const int *>(psb[f] + at);
+    };
+
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int f = 0; f < FN; ++f) acc[i][f] = (f32x4)0.0f;
+    i32x8 af[2][2], bf[FN];
+    [[maybe_unused]] Wide bw[EXACT ? FN : 1];
+
+    // step s, whose operands are in (as, bs) and the next one's in (an, bn)
+    const auto step = [&](auto par, uint32_t s, uint8_t *as, uint8_t *bs, uint8_t *an, uint8_t *bn) {
+        constexpr int S = decltype(par)::value;
+#pragma unroll
+        for (int ag = 0; ag < NG; ++ag) {
+            constexpr int P0 = (S * NG) & 1;
+            const int cur = (P0 + ag) & 1;
+            if (ag + 1 < NG) {
+                af[cur ^ 1][0] = read_a(as, 2 * ag + 2);
+                af[cur ^ 1][1] = read_a(as, 2 * ag + 3);
+            } else {
+                __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's LDS reads and copies are done
+                __syncthreads();
+                if (partial_chunk && s + 2 == s1) clear_tail(an, bn);
+                copy(s + 2, as, bs);
+                af[cur ^ 1][0] = read_a(an, 0);
+                af[cur ^ 1][1] = read_a(an, 1);
+            }
+if constexpr (EXACT) {
+                if (ag == 0) {
+#pragma unroll
+                    for (int f = 0; f < FN; ++f) bw[f] = widen(bf[f], scale_of<S>(sb[BLOCKS ? 0 : f]));
+                }
+                const Wide a0 = widen(af[cur][0], scale_of<S>(sa[2 * ag]));
+                const Wide a1 = widen(af[cur][1], scale_of<S>(sa[2 * ag + 1]));
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    acc[2 * ag][f] = mfma_wide(bw[f], a0, acc[2 * ag][f]);
+                    acc[2 * ag + 1][f] = mfma_wide(bw[f], a1, acc[2 * ag + 1][f]);
+                    if (ag + 1 == NG) bf[f] = read_b(bn, f);
+                }
+            } else {
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = 2 * ag + h;
+                        acc[i][f] = mfma<S>(bf[f], af[cur][h], acc[i][f], sb[BLOCKS ? 0 : f], sa[i]);
+                    }
+                    if (ag + 1 == NG) bf[f] = read_b(bn, f);
+                }
+            }
+        }
+    };
+    const auto next_scales = [&] {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sa[i] = na[i];
+#pragma unroll
+        for (int f = 0; f < NB; ++f) sb[f] = nb[f];
+    };
+
+    load_scales(s0, sa, sb);
+    copy(s0, as0, bs0);
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __syncthreads();
+    if (partial_chunk && steps == 1) clear_tail(as0, bs0);
+    copy(s0 + 1, as1, bs1);
+    af[0][0] = read_a(as0, 0);
+    af[0][1] = read_a(as0, 1);
+#pragma unroll
+    for (int f = 0; f < FN; ++f) bf[f] = read_b(bs0, f);
+    uint32_t s = s0;
+    for (; s + 4 <= s1; s += 4) {
+        step(std::integral_constant<int, 0>{}, s, as0, bs0, as1, bs1);
+        load_scales(s + 4, na, nb);
+        step(std::integral_constant<int, 1>{}, s + 1, as1, bs1, as0, bs0);
+        step(std::integral_constant<int, 2>{}, s + 2, as0, bs0, as1, bs1);
+        step(std::integral_constant<int, 3>{}, s + 3, as1, bs1, as0, bs0);
+        next_scales();
+    }
+    if (s < s1) step(std::integral_constant<int, 0>{}, s, as0, bs0, as1, bs1);
+    if (s + 1 < s1) step(std::integral_constant<int, 1>{}, s + 1, as1, bs1, as0, bs0);
+    if (s + 2 < s1) step(std::integral_constant<int, 2>{}, s + 2, as0, bs0, as1, bs1);
+
+    void *const out = p.out_dtype == kF32 ? (void *)((float *)p.out + split * p.split_stride) : p.out;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const uint32_t row = m0 + wm * FM * 16 + i * 16 + r;
+        if (row >= p.m) continue;
+#pragma unroll
+        for (int q = 0; q < FN / FB; ++q) {
+            const uint32_t c = n0 + wn * FN * 16 + q * 16 * FB + g * 4 * FB;
+#pragma unroll
+            for (int h = 0; h < FB / 2; ++h) {
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = acc[i][q * FB + 2 * h + (e >> 2)][e & 3];
+                put_out(out, p.out_dtype, row, p.out_stride, c + 8 * h, p.n, o);
+            }
+        }
+    }
+}
+
+// The splits' partial products, joined in order.
+__global__ __launch_bounds__(256) void join_splits(const float *__restrict__ part, uint32_t splits, uint64_t split_stride,
+                                                   uint32_t n8, uint32_t n, uint64_t count, void *out,
+                                                   uint64_t out_stride, int dtype)
+{
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (uint64_t)gridDim.x * 256) {
+        const uint64_t row = i / n8;
+        const uint32_t c = (uint32_t)(i - row * n8) * 8;
+        float f[8] = {};
+        for (uint32_t s = 0; s < splits; ++s) {
+            const auto v = load8<kF32>(part + s * split_stride + row * n, c, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] += v[e];
+        }
+        put_out(out, dtype, row, out_stride, c, n, f);
+    }
+}
+
+// Few rows of A (16 MT at most): B is read once and bounds the time. A
+// workgroup has 16 columns of the output; its W waves take runs of steps of
+// k, four steps' loads in flight, straight into registers, and add their
+// sums through LDS.
+template <int MT, int W, bool BLOCKS, bool EXACT>
+__global__ __launch_bounds__(W * 64) void gemm_rows(TileParams p)
+{
+    constexpr int U = MT <= 2 ? 4 : 2;  // steps in flight
+    __shared__ f32x4 sums[W][MT][64];
+    const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r = lane & 15u, g = lane >> 4;
+    const uint32_t n0 = blockIdx.x * 16;
+    const uint32_t steps = (p.k + kStep - 1) / kStep;
+    const uint32_t s0 = w * p.steps_per_split < steps ? w * p.steps_per_split : steps;
+    const uint32_t s1 = s0 + p.steps_per_split < steps ? s0 + p.steps_per_split : steps;
+    const auto ra = buffer_of(p.a), rb = buffer_of(p.b + (uint64_t)n0 * p.b_stride);
+    const uint32_t nr = n0 + r < p.n ? r : p.n - 1 - n0;
+    const uint32_t vb = nr * p.b_stride + g * 16;
+    uint32_t va[MT];
+    const uint8_t *psa[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const uint32_t row = t * 16 + r < p.m ? t * 16 + r : p.m - 1;
+        va[t] = row * p.a_stride + g * 16;
+        psa[t] = p.a_scale + (uint64_t)row * p.a_scale_stride;
+    }
+    const uint8_t *const psb = p.b_scale + (uint64_t)(BLOCKS ? n0 / 128 : n0 + nr) * p.b_scale_stride;
+    f32x4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = (f32x4)0.0f;
+    // 16 bytes at k of a row whose first byte this lane reads at offset v
+    const auto load = [&](__amdgpu_buffer_rsrc_t rsrc, uint32_t v, uint32_t k0, uint32_t half) {
+        const uint32_t k = k0 + half * 64 + g * 16;
+        i32x4 x = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rsrc, k < p.k ? v + half * 64 : kOutside, k0, 0));
+        if (k < p.k && k + 16 > p.k) {  // bytes past k may hold anything
+            const uint32_t keep = p.k - k;
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) {
+                const uint32_t kq = keep > 4 * q ? keep - 4 * q : 0;
+                if (kq < 4) x[q] &= (int)((1u << (8 * kq)) - 1u);
+            }
+        }
+        return x;
+    };
+    for (uint32_t s = s0; s < s1; s += U) {
+        int sa[MT], sb = *reinterpret_cast<const int *>(psb + (s & ~3u));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) sa[t] = *reinterpret_cast<const int *>(psa[t] + (s & ~3u));
+        i32x8 b[U], a[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t k0 = (s + u) * kStep;  // past the last step: zeros or a neighbour's, not multiplied
+            b[u] = join(load(rb, vb, k0, 0), load(rb, vb, k0, 1));
+#pragma unroll
+            for (int t = 0; t < MT; ++t) a[u][t] = join(load(ra, va[t], k0, 0), load(ra, va[t], k0, 1));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (s + u >= s1) break;
+            const uint32_t sh = 8 * ((s + u) & 3u);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if constexpr (EXACT)
+                    acc[t] = mfma_wide(widen(b[u], scale_of<0>(sb >> sh)), widen(a[u][t], scale_of<0>(sa[t] >> sh)), acc[t]);
+                else acc[t] = mfma<0>(b[u], a[u][t], acc[t], sb >> sh, sa[t] >> sh);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) sums[w][t][lane] = acc[t];
+    __syncthreads();
+    // lane l of fragment t has row 16 t + l % 16, columns 4 (l / 16) + e
+    for (uint32_t i = threadIdx.x; i < MT * 256; i += W * 64) {
+        const uint32_t t = i >> 8, row = t * 16 + ((i >> 4) & 15u), c = i & 15u;
+        float f = 0.0f;
+#pragma unroll
+        for (int q = 0; q < W; ++q) f += sums[q][t][((c >> 2) << 4) | ((i >> 4) & 15u)][c & 3u];
+        if (row < p.m && n0 + c < p.n) {
+            const uint64_t at = row * p.out_stride + n0 + c;
+            if (p.out_dtype == kBF16) ((uint16_t *)p.out)[at] = Elem<kBF16>::put(f);
+            else if (p.out_dtype == kF16) ((uint16_t *)p.out)[at] = Elem<kF16>::put(f);
+            else ((float *)p.out)[at] = f;
+        }
+    }
+}
+
+// How a product is cut: the rows kernel, or tiles of 32 f x 32 f and splits
+// of k.
+struct Cut {
+    int rows;  // > 0: the rows kernel with this many fragments of A
+    int f;
+    uint32_t splits, steps_per_split;
+};
+
+Cut cut_of(uint64_t m, uint64_t n, uint64_t k, bool exact)
+{
+    const uint32_t steps = (uint32_t)div_up(k, kStep);
+    Cut best{};
+    if (m <= 64) {
+        best.rows = m <= 16 ? 1 : m <= 32 ? 2 : 4;
+        best.splits = 1;
+        const uint32_t waves = best.rows == 1 ? 16 : 8;
+        best.steps_per_split = (uint32_t)(div_up(div_up(steps, waves), 4) * 4);  // scales are read four steps at a time
+        return best;
+    }
+    // time of each cut in cycles of one compute unit: rounds of workgroups
+    // times their steps, the work of a step by tile size, a start and an end
+    // per workgroup, and the pass that joins splits
+    double least = 0;
+    const struct { int f; double step, ends; uint32_t per_cu; } kinds[] = {
+        {8, 2700, 6000, 1}, {4, 900, 4000, 2}, {2, 330, 3000, 4}};
+    for (const auto &t : kinds) {
+        if (exact && t.f == 8) continue;  // its accumulators leave no room for the widened operands
+        const double step = exact ? 2 * t.step : t.step;
+        const uint64_t tiles = div_up(m, 32u * t.f) * div_up(n, 32u * t.f);
+        for (uint32_t want = 1; want <= 16; want *= 2) {
+            const uint32_t per = (uint32_t)(div_up(div_up(steps, want), 4) * 4);
+            const uint32_t splits = (uint32_t)div_up(steps, per);
+            if (want > 1 && (per < 8 || splits != want)) continue;
+            if (tiles * splits >= (1u << 24)) continue;  // a launch has fewer than 2^32 threads
+            const uint64_t wgs = tiles * splits;
+            const uint64_t full = wgs / (256 * t.per_cu), rest = wgs % (256 * t.per_cu);
+            // a last round that does not fill the units runs fewer workgroups on each
+            const double share = rest ? (double)div_up(rest, 256) : 0;
+            double cost = (full * t.per_cu + share) * per * step + (full + (rest ? 1 : 0)) * t.ends;
+            if (splits > 1) cost += 8000 + (double)m * n * 4 * (splits + 1) / 2000;
+            if (best.f == 0 || cost < least) {
+                least = cost;
+                best.f = t.f;
+                best.splits = splits;
+                best.steps_per_split = per;
+            }
+        }
+    }
+    return best;
+}
+
+template <int F, bool BLOCKS, bool EXACT>
+void launch_tile(const TileParams &p, uint32_t blocks, hipStream_t stream)
+{
+    if (p.k % kStep) gemm_tile<F, F, BLOCKS, true, EXACT><<<blocks, 256, 0, stream>>>(p);
+    else gemm_tile<F, F, BLOCKS, false, EXACT><<<blocks, 256, 0, stream>>>(p);
+}
+
+template <bool BLOCKS, bool EXACT>
+hipError_t launch_gemm(const GemmArgs &g)
+{
+    const Cut c = cut_of(g.m, g.n, g.k, EXACT);
+    TileParams p{};
+    p.a = g.a;
+    p.a_scale = g.a_scale;
+    p.b = g.b;
+    p.b_scale = g.b_scale;
+    p.a_stride = (uint32_t)g.a_stride;
+    p.a_scale_stride = (uint32_t)g.a_scale_stride;
+    p.b_stride = (uint32_t)g.b_stride;
+    p.b_scale_stride = (uint32_t)g.b_scale_stride;
+    p.m = (uint32_t)g.m;
+    p.n = (uint32_t)g.n;
+    p.k = (uint32_t)g.k;
+    p.steps_per_split = c.steps_per_split;
+    p.out = g.out;
+    p.out_stride = g.out_stride;
+    p.out_dtype = g.out_dtype;
+    if (c.rows) {
+        const uint32_t blocks = (uint32_t)div_up(g.n, 16);
+        if (c.rows == 1) gemm_rows<1, 16, BLOCKS, EXACT><<<blocks, 1024, 0, g.stream>>>(p);
+        else if (c.rows == 2) gemm_rows<2, 8, BLOCKS, EXACT><<<blocks, 512, 0, g.stream>>>(p);
+        else gemm_rows<4, 8, BLOCKS, EXACT><<<blocks, 512, 0, g.stream>>>(p);
+        return hipGetLastError();
+    }
+    p.tiles_m = (uint32_t)div_up(g.m, 32u * c.f);
+    p.tiles_n = (uint32_t)div_up(g.n, 32u * c.f);
+    if (c.splits > 1) {
+        p.out = g.workspace;
+        p.out_stride = g.n;
+        p.split_stride = g.m * g.n;
+        p.out_dtype = kF32;
+    }
+    const uint32_t blocks = p.tiles_m * p.tiles_n * c.splits;
+    if (c.f == 4) launch_tile<4, BLOCKS, EXACT>(p, blocks, g.stream);
+    else if (c.f == 2) launch_tile<2, BLOCKS, EXACT>(p, blocks, g.stream);
+    else if constexpr (!EXACT) launch_tile<8, BLOCKS, EXACT>(p, blocks, g.stream);
+    if (c.splits > 1) {
+        const uint64_t n8 = div_up(g.n, 8), count = g.m * n8;
+        const uint64_t wgs = div_up(count, 256);
+        join_splits<<<(uint32_t)(wgs < 8192 ? wgs : 8192), 256, 0, g.stream>>>(
+            (const float *)g.workspace, c.splits, p.split_stride, (uint32_t)n8, (uint32_t)g.n, count, g.out,
+            g.out_stride, g.out_dtype);
+    }
+    return hipGetLastError();
+}
+
+__global__ __launch_bounds__(256) void zero_out(void *out, int dtype, uint64_t stride, uint32_t n8, uint32_t n,
+                                                uint64_t count)
+{
+    const float f[8] = {};
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (uint64_t)gridDim.x * 256)
+        put_out(out, dtype, i / n8, stride, (uint32_t)(i % n8) * 8, n, f);
+}
+
+}  // namespace
+
+uint64_t gemm_fp8_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int out_dtype)
+{
+    const Cut c = cut_of(m, n, k, out_dtype == kF32);
+    return c.splits > 1 ? 4ull * c.splits * m * n : 0;
+}
+
+hipError_t gemm_fp8(const GemmArgs &g)
+{
+    if (g.k == 0) {  // an empty sum
+        const uint64_t n8 = div_up(g.n, 8), count = g.m * n8, wgs = div_up(count, 256);
+        zero_out<<<(uint32_t)(wgs < 8192 ? wgs : 8192), 256, 0, g.stream>>>(g.out, g.out_dtype, g.out_stride,
+                                                                           (uint32_t)n8, (uint32_t)g.n, count);
+        return hipGetLastError();
+    }
+    if (g.out_dtype == kF32) return g.b_blocks ? launch_gemm<true, true>(g) : launch_gemm<false, true>(g);
+    return g.b_blocks ? launch_gemm<true, false>(g) : launch_gemm<false, false>(g);
+}
+
+}  // namespace cpk

@@ -1,0 +1,204 @@
+// cp_quant.hip - the 8-bit form of a matrix, and of its transpose.
+//
+// A group of 128 values (or a block of 128 x 128) with largest finite
+// magnitude A is stored as e4m3 values x / 2^e and the exponent e, the least
+// with A / 2^e <= 448.
+//
+// Bound by memory: the matrix is read once, in tiles of 128 x 128 that hold
+// whole groups of both directions, and both outputs are written from it.
+#include "cp_ops_internal.h"
+
+namespace cpk {
+
+namespace {
+
+constexpr uint32_t kTile = 128;
+
+// 8 bytes of a row, or those of them before its end (left = bytes to there).
+__device__ __forceinline__ void put8(uint8_t *p, u32x2 v, uint32_t left)
+{
+    if (left >= 8) {
+        *reinterpret_cast<u32x2 *>(p) = v;
+    } else {
+        for (uint32_t e = 0; e < left; ++e) p[e] = (uint8_t)(v[e >> 2] >> (8 * (e & 3u)));
+    }
+}
+
+// One tile per workgroup of 256 threads. Thread t has rows 8 (t / 16) + i
+// and columns 8 (t % 16) + e, i, e < 8: 16 neighbouring lanes hold a row's
+// 128 columns (a row of lanes, so its maximum needs no LDS), and a thread
+// holds 8 values that follow one another in either direction.
+//
+// The transposed tile goes through LDS, 128 rows (the tile's columns) of 128
+// bytes, in pieces of 8 bytes; piece p of row c stands at p ^ (c / 8 % 16),
+// so that the 16 lanes that store together, with columns 8 apart, hit
+// different banks.
+template <int DT, bool BLOCKS, bool TRANS>
+__global__ __launch_bounds__(256) void quantize_tile(const typename Elem<DT>::raw *__restrict__ x, uint32_t n,
+                                                     uint32_t d, uint64_t x_stride, uint32_t tiles_x,
+                                                     uint8_t *__restrict__ q, uint64_t q_stride,
+                                                     uint8_t *__restrict__ scale, uint64_t scale_stride,
+                                                     uint8_t *__restrict__ qt, uint64_t qt_stride,
+                                                     uint8_t *__restrict__ scale_t, uint64_t scale_t_stride)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t lds[TRANS ? kTile * kTile : 16];
+    __shared__ uint32_t part[4][kTile];
+    const uint32_t tx = blockIdx.x % tiles_x, ty = blockIdx.x / tiles_x;
+    const uint32_t cl = (threadIdx.x & 15u) * 8u, rl = (threadIdx.x >> 4) * 8u, wave = threadIdx.x >> 6;
+    const uint32_t c0 = tx * kTile + cl, r0 = ty * kTile + rl;
+    typename Elem<DT>::vec8 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (r0 + i < n) v[i] = load8<DT>(x + (r0 + i) * x_stride, c0, d);
+        else v[i] = (typename Elem<DT>::raw)0;
+    }
+    // largest magnitudes: of each row's 8 columns and each column's 8 rows
+    uint32_t mr[8], mc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mr[i] = mc[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = finite_bits(Elem<DT>::get(v[i][e]));
+            mr[i] = mr[i] > b ? mr[i] : b;
+            if constexpr (TRANS && !BLOCKS) mc[e] = mc[e] > b ? mc[e] : b;
+        }
+    }
+    uint32_t byte_r[8], byte_c[8];
+    if constexpr (BLOCKS) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = m > mr[i] ? m : mr[i];
+        m = max_of_16(m);
+        uint32_t o = (uint32_t)__shfl_xor((int)m, 16, 64);
+        m = m > o ? m : o;
+        o = (uint32_t)__shfl_xor((int)m, 32, 64);
+        m = m > o ? m : o;
+        if ((threadIdx.x & 63u) == 0) part[wave][0] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = m > part[w][0] ? m : part[w][0];
+        byte_r[0] = scale_byte(m);
+        if (threadIdx.x == 0) {
+            scale[ty * scale_stride + tx] = (uint8_t)byte_r[0];
+            if constexpr (TRANS) scale_t[tx * scale_t_stride + ty] = (uint8_t)byte_r[0];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            byte_r[i] = scale_byte(max_of_16(mr[i]));
+            if ((threadIdx.x & 15u) == 0 && r0 + i < n) scale[(r0 + i) * scale_stride + tx] = (uint8_t)byte_r[i];
+        }
+        if constexpr (TRANS) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                uint32_t o = (uint32_t)__shfl_xor((int)mc[e], 16, 64);
+                mc[e] = mc[e] > o ? mc[e] : o;
+                o = (uint32_t)__shfl_xor((int)mc[e], 32, 64);
+                mc[e] = mc[e] > o ? mc[e] : o;
+                if ((threadIdx.x & 63u) < 16) part[wave][cl + e] = mc[e];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                uint32_t m = part[0][cl + e];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) m = m > part[w][cl + e] ? m : part[w][cl + e];
+                byte_c[e] = scale_byte(m);
+            }
+            if (threadIdx.x < 16) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c0 + e < d) scale_t[(c0 + e) * scale_t_stride + ty] = (uint8_t)byte_c[e];
+            }
+        }
+    }
+    const uint32_t left = c0 < d ? d - c0 : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float inv = inverse_scale(byte_r[BLOCKS ? 0 : i]);
+        u32x2 o;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            o[h] = to_e4m3x4(Elem<DT>::get(v[i][4 * h]), Elem<DT>::get(v[i][4 * h + 1]),
+                             Elem<DT>::get(v[i][4 * h + 2]), Elem<DT>::get(v[i][4 * h + 3]), inv);
+        if (r0 + i < n) put8(q + (r0 + i) * q_stride + c0, o, left);
+    }
+    if constexpr (TRANS) {
+        // column e's 8 rows: piece rl / 8 of LDS row cl + e
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float inv = inverse_scale(BLOCKS ? byte_r[0] : byte_c[e]);
+            u32x2 o;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                o[h] = to_e4m3x4(Elem<DT>::get(v[4 * h][e]), Elem<DT>::get(v[4 * h + 1][e]),
+                                 Elem<DT>::get(v[4 * h + 2][e]), Elem<DT>::get(v[4 * h + 3][e]), inv);
+            const uint32_t piece = (rl >> 3) ^ (cl >> 3);
+            *reinterpret_cast<u32x2 *>(lds + (cl + e) * kTile + piece * 8u) = o;
+        }
+        __syncthreads();
+        // 8 lanes write an output row's 128 bytes, 16 at a time
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = i * 32u + (threadIdx.x >> 3), p = (threadIdx.x & 7u) * 2u, sw = (c >> 3) & 15u;
+            if (tx * kTile + c >= d) continue;
+            const u32x2 a = *reinterpret_cast<const u32x2 *>(lds + c * kTile + (p ^ sw) * 8u);
+            const u32x2 b = *reinterpret_cast<const u32x2 *>(lds + c * kTile + ((p + 1) ^ sw) * 8u);
+            uint8_t *const to = qt + (uint64_t)(tx * kTile + c) * qt_stride + ty * kTile + p * 8u;
+            const uint32_t at = ty * kTile + p * 8u;
+            if (at + 16 <= n) {
+                u32x4 o;
+                o[0] = a[0];
+                o[1] = a[1];
+                o[2] = b[0];
+                o[3] = b[1];
+                *reinterpret_cast<u32x4 *>(to) = o;
+            } else if (at < n) {
+                put8(to, a, n - at);
+                if (at + 8 < n) put8(to + 8, b, n - at - 8);
+            }
+        }
+    }
+}
+
+template <int DT, bool BLOCKS, bool TRANS>
+hipError_t launch(const QuantArgs &a)
+{
+    const uint64_t tiles_x = div_up(a.d, kTile);
+    // whole rows of tiles per launch, fewer than 2^32 threads in each
+    uint64_t step = (1ull << 23) / tiles_x;
+    if (step == 0) step = 1;
+    const uint64_t tiles_y = div_up(a.n, kTile);
+    for (uint64_t y = 0; y < tiles_y; y += step) {
+        const uint64_t r = y * kTile, ny = tiles_y - y < step ? tiles_y - y : step;
+        const uint64_t n = a.n - r < ny * kTile ? a.n - r : ny * kTile;
+        quantize_tile<DT, BLOCKS, TRANS><<<(uint32_t)(ny * tiles_x), 256, 0, a.stream>>>(
+            (const typename Elem<DT>::raw *)a.x + r * a.x_stride, (uint32_t)n, (uint32_t)a.d, a.x_stride,
+            (uint32_t)tiles_x, a.q + r * a.q_stride, a.q_stride, a.scale + (BLOCKS ? y : r) * a.scale_stride,
+            a.scale_stride, TRANS ? a.qt + r : nullptr, a.qt_stride, TRANS ? a.scale_t + y : nullptr,
+            a.scale_t_stride);
+    }
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t quant_of(const QuantArgs &a)
+{
+    if (a.blocks) return a.qt ? launch<DT, true, true>(a) : launch<DT, true, false>(a);
+    return a.qt ? launch<DT, false, true>(a) : launch<DT, false, false>(a);
+}
+
+}  // namespace
+
+hipError_t quantize_fp8(const QuantArgs &a)
+{
+    switch (a.dtype) {
+    case kF32: return quant_of<kF32>(a);
+    case kBF16: return quant_of<kBF16>(a);
+    default: return quant_of<kF16>(a);
+    }
+}
+
+}  // namespace cpk
