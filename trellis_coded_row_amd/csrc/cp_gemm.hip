@@ -30,11 +30,12 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr uint32_t kStep = 128;              // values of k per step (one scale group)
-constexpr uint32_t kOutside = 0x80000000u;   // a buffer offset past any tile: loads give zeros
+constexpr uint32_t kInside = 0x7FFFFFFFu;    // bytes of a buffer: any offset within a tile
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past it: loads give zeros
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t size = kInside)
 {
-    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, 0x7FFFFFFF, 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)size, 0x00020000);
 }
 
 // The scales are byte S of sb and sa.
@@ -43,6 +44,31 @@ __device__ __forceinline__ f32x4 mfma(i32x8 b, i32x8 a, f32x4 c, int sb, int sa)
 {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, c, 0, 0, S, sb, S, sa);
 }
+
+// The same with the accumulator held in one place: left to itself, the
+// compiler gives the largest tile's products a result register other than
+// the one they add to, and with 256 accumulators there is none to spare.
+// Bytes 0 and 1 only. The s_nop covers the wait that a preceding vector
+// instruction's write to an operand needs, which the compiler does not count
+// for assembly; it runs under the previous product. Results may be read
+// after settle().
+template <int S>
+__device__ __forceinline__ void mfma_in_place(f32x4 &c, i32x8 b, i32x8 a, int sb, int sa)
+{
+    static_assert(S == 0 || S == 1, "");
+    if constexpr (S == 0)
+        asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                     : "+a"(c)
+                     : "v"(b), "v"(a), "v"(sb), "v"(sa));
+    else
+        asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] "
+                     "op_sel_hi:[0,0,0]"
+                     : "+a"(c)
+                     : "v"(b), "v"(a), "v"(sb), "v"(sa));
+}
+
+// Waits until the last product's result can be read.
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15"); }
 
 __device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi)
 {
@@ -130,6 +156,7 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
 {
     constexpr uint32_t BM = 32 * FM, BN = 32 * FN;
     constexpr int FB = FN < 4 ? FN : 4, NG = FM / 2;
+    constexpr bool IN_PLACE = !EXACT && FM * FN == 64;
     constexpr int LA = BM / 32, LB = BN / 32;  // copies of 8 rows per wave
     __shared__ __attribute__((aligned(16))) uint8_t as0[BM * kStep], as1[BM * kStep], bs0[BN * kStep],
         bs1[BN * kStep];
@@ -141,17 +168,19 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
     const uint32_t ntiles = p.tiles_m * p.tiles_n, total = gridDim.x;
     const uint32_t xcd = blockIdx.x & 7u, per = total >> 3, extra = total & 7u;
     const uint32_t id = xcd * per + (xcd < extra ? xcd : extra) + (blockIdx.x >> 3);
-    const uint32_t split = id / ntiles, tile = id % ntiles;
-    const uint32_t band = tile / (8 * p.tiles_n), band_m = band * 8;
+    // (the quotients come out of vector registers: back to scalar ones)
+    const uint32_t split = __builtin_amdgcn_readfirstlane(id / ntiles), tile = id - split * ntiles;
+    const uint32_t band = __builtin_amdgcn_readfirstlane(tile / (8 * p.tiles_n)), band_m = band * 8;
     const uint32_t band_rows = p.tiles_m - band_m < 8 ? p.tiles_m - band_m : 8;
     const uint32_t in_band = tile - band * 8 * p.tiles_n;
-    const uint32_t m0 = (band_m + in_band % band_rows) * BM, n0 = (in_band / band_rows) * BN;
+    const uint32_t column = __builtin_amdgcn_readfirstlane(in_band / band_rows);
+    const uint32_t m0 = (band_m + in_band - column * band_rows) * BM, n0 = column * BN;
     const uint32_t all_steps = (p.k + kStep - 1) / kStep;
     const uint32_t s0 = split * p.steps_per_split;
     const uint32_t s1 = s0 + p.steps_per_split < all_steps ? s0 + p.steps_per_split : all_steps;
     const uint32_t steps = s1 - s0;
 
-    const auto ra = buffer_of(p.a + (uint64_t)m0 * p.a_stride), rb = buffer_of(p.b + (uint64_t)n0 * p.b_stride);
+    const uint8_t *const pa = p.a + (uint64_t)m0 * p.a_stride, *const pb = p.b + (uint64_t)n0 * p.b_stride;
     // where this lane's part of each copy comes from (rows past the end: the last one)
     uint32_t va[LA], vb[LB], ca[LA], cb[LB];
 #pragma unroll
@@ -166,18 +195,27 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
         cb[i] = ((lane & 7u) ^ (((row / (4 * FB)) & 3u) << 1 | ((row >> 1) & 1u))) * 16;
         vb[i] = in * p.b_stride + cb[i];
     }
-    const auto copy = [&](uint32_t s, uint8_t *as, uint8_t *bs) {
-        const uint32_t k0 = (s < s1 ? s : s1 - 1) * kStep;  // past the end: the last step again, never read
+    // this wave's copies of 8 rows, j of FN shares
+    const auto copy_share = [&](uint32_t s, uint8_t *as, uint8_t *bs, int j) {
+        const uint32_t k0 = s * kStep;
+        const uint32_t size = s < s1 ? kInside : 0;  // past the last step: zeros
+        const auto ra = buffer_of(pa, size), rb = buffer_of(pb, size);
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
+            if (i % FN != j) continue;
             const uint32_t v = KTAIL && k0 + ca[i] >= p.k ? kOutside : va[i];
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(as + (w * LA + i) * 1024), 16, v, k0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < LB; ++i) {
+            if (i % FN != j) continue;
             const uint32_t v = KTAIL && k0 + cb[i] >= p.k ? kOutside : vb[i];
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(bs + (w * LB + i) * 1024), 16, v, k0, 0, 0);
         }
+    };
+    const auto copy = [&](uint32_t s, uint8_t *as, uint8_t *bs) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) copy_share(s, as, bs, j);
     };
     // k ends inside a chunk: its bytes past k, which may hold anything, are
     // cleared in LDS
@@ -210,26 +248,28 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
     // scales: a dword has a row's bytes for four steps; one row of scales for
     // a wave's columns where they are for blocks
     constexpr int NB = BLOCKS ? 1 : FN;
-    const uint8_t *psa[FM], *psb[NB];
+    const uint8_t *const qa = p.a_scale + (uint64_t)m0 * p.a_scale_stride;
+    const uint8_t *const qb = p.b_scale + (uint64_t)(BLOCKS ? n0 / 128 : n0) * p.b_scale_stride;
+    uint32_t va_scale[FM], vb_scale[NB];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const uint32_t row = m0 + wm * FM * 16 + i * 16 + r;
-        psa[i] = p.a_scale + (uint64_t)(row < p.m ? row : p.m - 1) * p.a_scale_stride;
+        const uint32_t row = wm * FM * 16 + i * 16 + r;
+        va_scale[i] = (m0 + row < p.m ? row : p.m - 1 - m0) * p.a_scale_stride;
     }
 #pragma unroll
     for (int f = 0; f < NB; ++f) {
-        const uint32_t c0 = n0 + wn * FN * 16;
-        uint32_t row = BLOCKS ? c0 : c0 + (f / FB) * 16 * FB + (r >> 2) * (4 * FB) + (f % FB) * 4 + (r & 3u);
-        row = row < p.n ? row : p.n - 1;
-        psb[f] = p.b_scale + (uint64_t)(BLOCKS ? row / 128 : row) * p.b_scale_stride;
+        const uint32_t first = wn * FN * 16;
+        uint32_t row = BLOCKS ? first : first + (f / FB) * 16 * FB + (r >> 2) * (4 * FB) + (f % FB) * 4 + (r & 3u);
+        row = n0 + row < p.n ? row : p.n - 1 - n0;
+        vb_scale[f] = (BLOCKS ? (n0 + row) / 128 - n0 / 128 : row) * p.b_scale_stride;
     }
-    int sa[FM], sb[NB], na[FM], nb[NB];
+    int sa[FM], sb[NB], ha[FM], hb[NB], na[FM], nb[NB];  // this pair of steps', these four steps', the next four's
     const auto load_scales = [&](uint32_t s, int *ta, int *tb) {
-        const uint32_t at = (s < s1 ? s : s1 - 1) & ~3u;
+        const uint32_t at = s < s1 ? s : s0;
 #pragma unroll
-        for (int i = 0; i < FM; ++i) ta[i] = *reinterpret_cast<const int *>(psa[i] + at);
+        for (int i = 0; i < FM; ++i) ta[i] = *reinterpret_cast<const int *>(qa + at + va_scale[i]);
 #pragma unroll
-        for (int f = 0; f < NB; ++f) tb[f] = *reinterpret_cast<const int *>(psb[f] + at);
+        for (int f = 0; f < NB; ++f) tb[f] = *reinterpret_cast<const int *>(qb + at + vb_scale[f]);
     };
 
     f32x4 acc[FM][FN];
@@ -254,7 +294,7 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
                 __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's LDS reads and copies are done
                 __syncthreads();
                 if (partial_chunk && s + 2 == s1) clear_tail(an, bn);
-                copy(s + 2, as, bs);
+                if constexpr (EXACT) copy(s + 2, as, bs);
                 af[cur ^ 1][0] = read_a(an, 0);
                 af[cur ^ 1][1] = read_a(an, 1);
             }
@@ -274,24 +314,29 @@ if constexpr (EXACT) {
             } else {
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
+                    if (ag + 1 == NG) copy_share(s + 2, as, bs, f);  // one share before each pair of products
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int i = 2 * ag + h;
-                        acc[i][f] = mfma<S>(bf[f], af[cur][h], acc[i][f], sb[BLOCKS ? 0 : f], sa[i]);
+                        if constexpr (IN_PLACE) mfma_in_place<S>(acc[i][f], bf[f], af[cur][h], sb[BLOCKS ? 0 : f], sa[i]);
+                        else acc[i][f] = mfma<S>(bf[f], af[cur][h], acc[i][f], sb[BLOCKS ? 0 : f], sa[i]);
                     }
-                    if (ag + 1 == NG) bf[f] = read_b(bn, f);
+                    if (ag + 1 == NG) {
+                        bf[f] = read_b(bn, f);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
             }
+            // keep the group's products here: left alone, the compiler moves
+            // them down to the loop's end, with every operand live until there
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int f = 0; f < FN; ++f) asm volatile("" : "+a"(acc[2 * ag + h][f]));
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    const auto next_scales = [&] {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) sa[i] = na[i];
-#pragma unroll
-        for (int f = 0; f < NB; ++f) sb[f] = nb[f];
-    };
-
-    load_scales(s0, sa, sb);
+    load_scales(s0, ha, hb);
     copy(s0, as0, bs0);
     __builtin_amdgcn_s_waitcnt(0x0070);
     __syncthreads();
@@ -301,19 +346,35 @@ if constexpr (EXACT) {
     af[0][1] = read_a(as0, 1);
 #pragma unroll
     for (int f = 0; f < FN; ++f) bf[f] = read_b(bs0, f);
+    // two steps a turn, the second of an odd number on zeros; s0 is a multiple of 4
     uint32_t s = s0;
-    for (; s + 4 <= s1; s += 4) {
+    do {
+        if ((s & 2u) == 0) load_scales(s + 4, na, nb);
+        // a step past k's end has no scale: 1 in place of what stands there
+        const uint32_t shift = (s & 2u) * 8;
+        const int keep = s + 1 < all_steps ? -1 : 0xFF, fill = s + 1 < all_steps ? 0 : 0x7F00;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sa[i] = ((ha[i] >> shift) & keep) | fill;
+#pragma unroll
+        for (int f = 0; f < NB; ++f) sb[f] = ((hb[f] >> shift) & keep) | fill;
         step(std::integral_constant<int, 0>{}, s, as0, bs0, as1, bs1);
-        load_scales(s + 4, na, nb);
         step(std::integral_constant<int, 1>{}, s + 1, as1, bs1, as0, bs0);
-        step(std::integral_constant<int, 2>{}, s + 2, as0, bs0, as1, bs1);
-        step(std::integral_constant<int, 3>{}, s + 3, as1, bs1, as0, bs0);
-        next_scales();
-    }
-    if (s < s1) step(std::integral_constant<int, 0>{}, s, as0, bs0, as1, bs1);
-    if (s + 1 < s1) step(std::integral_constant<int, 1>{}, s + 1, as1, bs1, as0, bs0);
-    if (s + 2 < s1) step(std::integral_constant<int, 2>{}, s + 2, as0, bs0, as1, bs1);
+        if (s & 2u) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i) ha[i] = na[i];
+#pragma unroll
+            for (int f = 0; f < NB; ++f) hb[f] = nb[f];
+        }
+        s += 2;
+    } while (s < s1);
 
+    if constexpr (IN_PLACE) {
+        settle();
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int f = 0; f < FN; ++f) asm volatile("" : "+a"(acc[i][f]));
+    }
     void *const out = p.out_dtype == kF32 ? (void *)((float *)p.out + split * p.split_stride) : p.out;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
