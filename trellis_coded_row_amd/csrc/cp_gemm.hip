@@ -278,7 +278,6 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
 #pragma unroll
         for (int f = 0; f < FN; ++f) acc[i][f] = (f32x4)0.0f;
     i32x8 af[2][2], bf[FN];
-    [[maybe_unused]] Wide bw[EXACT ? FN : 1];
 
     // step s, whose operands are in (as, bs) and the next one's in (an, bn)
     const auto step = [&](auto par, uint32_t s, uint8_t *as, uint8_t *bs, uint8_t *an, uint8_t *bn) {
@@ -294,37 +293,21 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
                 __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's LDS reads and copies are done
                 __syncthreads();
                 if (partial_chunk && s + 2 == s1) clear_tail(an, bn);
-                if constexpr (EXACT) copy(s + 2, as, bs);
                 af[cur ^ 1][0] = read_a(an, 0);
                 af[cur ^ 1][1] = read_a(an, 1);
             }
-if constexpr (EXACT) {
-                if (ag == 0) {
 #pragma unroll
-                    for (int f = 0; f < FN; ++f) bw[f] = widen(bf[f], scale_of<S>(sb[BLOCKS ? 0 : f]));
+            for (int f = 0; f < FN; ++f) {
+                if (ag + 1 == NG) copy_share(s + 2, as, bs, f);  // one share before each pair of products
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int i = 2 * ag + h;
+                    if constexpr (IN_PLACE) mfma_in_place<S>(acc[i][f], bf[f], af[cur][h], sb[BLOCKS ? 0 : f], sa[i]);
+                    else acc[i][f] = mfma<S>(bf[f], af[cur][h], acc[i][f], sb[BLOCKS ? 0 : f], sa[i]);
                 }
-                const Wide a0 = widen(af[cur][0], scale_of<S>(sa[2 * ag]));
-                const Wide a1 = widen(af[cur][1], scale_of<S>(sa[2 * ag + 1]));
-#pragma unroll
-                for (int f = 0; f < FN; ++f) {
-                    acc[2 * ag][f] = mfma_wide(bw[f], a0, acc[2 * ag][f]);
-                    acc[2 * ag + 1][f] = mfma_wide(bw[f], a1, acc[2 * ag + 1][f]);
-                    if (ag + 1 == NG) bf[f] = read_b(bn, f);
-                }
-            } else {
-#pragma unroll
-                for (int f = 0; f < FN; ++f) {
-                    if (ag + 1 == NG) copy_share(s + 2, as, bs, f);  // one share before each pair of products
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int i = 2 * ag + h;
-                        if constexpr (IN_PLACE) mfma_in_place<S>(acc[i][f], bf[f], af[cur][h], sb[BLOCKS ? 0 : f], sa[i]);
-                        else acc[i][f] = mfma<S>(bf[f], af[cur][h], acc[i][f], sb[BLOCKS ? 0 : f], sa[i]);
-                    }
-                    if (ag + 1 == NG) {
-                        bf[f] = read_b(bn, f);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                if (ag + 1 == NG) {
+                    bf[f] = read_b(bn, f);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
             // keep the group's products here: left alone, the compiler moves
@@ -336,16 +319,85 @@ if constexpr (EXACT) {
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    // The same step on widened operands: while a group's products run, the
+    // next group's fragments are widened and those of the one after it read.
+    [[maybe_unused]] Wide aw[2], bw[EXACT ? FN : 1];
+    [[maybe_unused]] i32x8 raw[2];
+    [[maybe_unused]] int pa_next[FM], pb_next[NB];  // the next pair of steps' scales
+    [[maybe_unused]] const auto step_wide = [&](auto par, uint32_t s, uint8_t *as, uint8_t *bs, uint8_t *an,
+                                                uint8_t *bn) {
+        constexpr int S = decltype(par)::value;
+        const auto next_a = [&](int i) { return S == 0 ? scale_of<1>(sa[i]) : scale_of<0>(pa_next[i]); };
+        const auto next_b = [&](int f) { return S == 0 ? scale_of<1>(sb[f]) : scale_of<0>(pb_next[f]); };
+#pragma unroll
+        for (int ag = 0; ag < NG; ++ag) {
+            i32x8 after[2], rb[FN];
+            if (ag + 1 < NG) {
+                if (ag + 2 < NG) {
+                    after[0] = read_a(as, 2 * ag + 4);
+                    after[1] = read_a(as, 2 * ag + 5);
+                }
+            } else {
+                __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's LDS reads and copies are done
+                __syncthreads();
+                if (partial_chunk && s + 2 == s1) clear_tail(an, bn);
+                raw[0] = read_a(an, 0);
+                raw[1] = read_a(an, 1);
+#pragma unroll
+                for (int f = 0; f < FN; ++f) rb[f] = read_b(bn, f);
+                if constexpr (NG > 1) {
+                    after[0] = read_a(an, 2);
+                    after[1] = read_a(an, 3);
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                if (ag + 1 == NG) copy_share(s + 2, as, bs, f);
+                acc[2 * ag][f] = mfma_wide(bw[f], aw[0], acc[2 * ag][f]);
+                acc[2 * ag + 1][f] = mfma_wide(bw[f], aw[1], acc[2 * ag + 1][f]);
+                if (ag + 1 == NG) bw[f] = widen(rb[f], next_b(BLOCKS ? 0 : f));
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                aw[h] = widen(raw[h], ag + 1 < NG ? scale_of<S>(sa[(2 * ag + 2 + h) % FM]) : next_a(h));
+                raw[h] = after[h];
+            }
+            // between products, their share of the conversions
+            if (ag + 1 < NG) {
+#pragma unroll
+                for (int q = 0; q < 8 * FN; ++q) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, (32 + 8 * FN - 1) / (8 * FN), 0);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int f = 0; f < FN; ++f) asm volatile("" : "+a"(acc[2 * ag + h][f]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
     load_scales(s0, ha, hb);
     copy(s0, as0, bs0);
     __builtin_amdgcn_s_waitcnt(0x0070);
     __syncthreads();
     if (partial_chunk && steps == 1) clear_tail(as0, bs0);
     copy(s0 + 1, as1, bs1);
-    af[0][0] = read_a(as0, 0);
-    af[0][1] = read_a(as0, 1);
+    if constexpr (EXACT) {
 #pragma unroll
-    for (int f = 0; f < FN; ++f) bf[f] = read_b(bs0, f);
+        for (int h = 0; h < 2; ++h) {
+            aw[h] = widen(read_a(as0, h), scale_of<0>(ha[h]));
+            if constexpr (NG > 1) raw[h] = read_a(as0, 2 + h);
+        }
+#pragma unroll
+        for (int f = 0; f < FN; ++f) bw[f] = widen(read_b(bs0, f), scale_of<0>(hb[BLOCKS ? 0 : f]));
+    } else {
+        af[0][0] = read_a(as0, 0);
+        af[0][1] = read_a(as0, 1);
+#pragma unroll
+        for (int f = 0; f < FN; ++f) bf[f] = read_b(bs0, f);
+    }
     // two steps a turn, the second of an odd number on zeros; s0 is a multiple of 4
     uint32_t s = s0;
     do {
@@ -357,8 +409,17 @@ if constexpr (EXACT) {
         for (int i = 0; i < FM; ++i) sa[i] = ((ha[i] >> shift) & keep) | fill;
 #pragma unroll
         for (int f = 0; f < NB; ++f) sb[f] = ((hb[f] >> shift) & keep) | fill;
-        step(std::integral_constant<int, 0>{}, s, as0, bs0, as1, bs1);
-        step(std::integral_constant<int, 1>{}, s + 1, as1, bs1, as0, bs0);
+        if constexpr (EXACT) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pa_next[i] = (s & 2u) ? na[i] : ha[i] >> 16;
+#pragma unroll
+            for (int f = 0; f < NB; ++f) pb_next[f] = (s & 2u) ? nb[f] : hb[f] >> 16;
+            step_wide(std::integral_constant<int, 0>{}, s, as0, bs0, as1, bs1);
+            step_wide(std::integral_constant<int, 1>{}, s + 1, as1, bs1, as0, bs0);
+        } else {
+            step(std::integral_constant<int, 0>{}, s, as0, bs0, as1, bs1);
+            step(std::integral_constant<int, 1>{}, s + 1, as1, bs1, as0, bs0);
+        }
         if (s & 2u) {
 #pragma unroll
             for (int i = 0; i < FM; ++i) ha[i] = na[i];
@@ -502,8 +563,8 @@ __global__ __launch_bounds__(W * 64) void gemm_rows(TileParams p)
 // How a product is cut: the rows kernel, or tiles of 32 f x 32 f and splits
 // of k.
 struct Cut {
-    int rows;  // > 0: the rows kernel with this many fragments of A
-    int f;
+    int rows;    // > 0: the rows kernel with this many fragments of A
+    int fm, fn;  // else tiles of 32 fm x 32 fn
     uint32_t splits, steps_per_split;
 };
 
@@ -522,12 +583,13 @@ Cut cut_of(uint64_t m, uint64_t n, uint64_t k, bool exact)
     // times their steps, the work of a step by tile size, a start and an end
     // per workgroup, and the pass that joins splits
     double least = 0;
-    const struct { int f; double step, ends; uint32_t per_cu; } kinds[] = {
-        {8, 2700, 6000, 1}, {4, 900, 4000, 2}, {2, 330, 3000, 4}};
-    for (const auto &t : kinds) {
-        if (exact && t.f == 8) continue;  // its accumulators leave no room for the widened operands
-        const double step = exact ? 2 * t.step : t.step;
-        const uint64_t tiles = div_up(m, 32u * t.f) * div_up(n, 32u * t.f);
+    struct Kind { int fm, fn; double step, ends; uint32_t per_cu; };
+    static const Kind narrow[] = {{8, 8, 2700, 6000, 1}, {4, 4, 900, 4000, 2}, {2, 2, 330, 3000, 4}};
+    static const Kind wide[] = {{8, 4, 2600, 6000, 1}, {4, 4, 1800, 4000, 2}, {2, 2, 660, 3000, 4}};
+    const Kind *const kinds = exact ? wide : narrow;
+    for (int q = 0; q < 3; ++q) {
+        const Kind &t = kinds[q];
+        const uint64_t tiles = div_up(m, 32u * t.fm) * div_up(n, 32u * t.fn);
         for (uint32_t want = 1; want <= 16; want *= 2) {
             const uint32_t per = (uint32_t)(div_up(div_up(steps, want), 4) * 4);
             const uint32_t splits = (uint32_t)div_up(steps, per);
@@ -537,11 +599,12 @@ Cut cut_of(uint64_t m, uint64_t n, uint64_t k, bool exact)
             const uint64_t full = wgs / (256 * t.per_cu), rest = wgs % (256 * t.per_cu);
             // a last round that does not fill the units runs fewer workgroups on each
             const double share = rest ? (double)div_up(rest, 256) : 0;
-            double cost = (full * t.per_cu + share) * per * step + (full + (rest ? 1 : 0)) * t.ends;
+            double cost = (full * t.per_cu + share) * per * t.step + (full + (rest ? 1 : 0)) * t.ends;
             if (splits > 1) cost += 8000 + (double)m * n * 4 * (splits + 1) / 2000;
-            if (best.f == 0 || cost < least) {
+            if (best.fm == 0 || cost < least) {
                 least = cost;
-                best.f = t.f;
+                best.fm = t.fm;
+                best.fn = t.fn;
                 best.splits = splits;
                 best.steps_per_split = per;
             }
@@ -550,11 +613,11 @@ Cut cut_of(uint64_t m, uint64_t n, uint64_t k, bool exact)
     return best;
 }
 
-template <int F, bool BLOCKS, bool EXACT>
+template <int FM, int FN, bool BLOCKS, bool EXACT>
 void launch_tile(const TileParams &p, uint32_t blocks, hipStream_t stream)
 {
-    if (p.k % kStep) gemm_tile<F, F, BLOCKS, true, EXACT><<<blocks, 256, 0, stream>>>(p);
-    else gemm_tile<F, F, BLOCKS, false, EXACT><<<blocks, 256, 0, stream>>>(p);
+    if (p.k % kStep) gemm_tile<FM, FN, BLOCKS, true, EXACT><<<blocks, 256, 0, stream>>>(p);
+    else gemm_tile<FM, FN, BLOCKS, false, EXACT><<<blocks, 256, 0, stream>>>(p);
 }
 
 template <bool BLOCKS, bool EXACT>
@@ -584,8 +647,8 @@ hipError_t launch_gemm(const GemmArgs &g)
         else gemm_rows<4, 8, BLOCKS, EXACT><<<blocks, 512, 0, g.stream>>>(p);
         return hipGetLastError();
     }
-    p.tiles_m = (uint32_t)div_up(g.m, 32u * c.f);
-    p.tiles_n = (uint32_t)div_up(g.n, 32u * c.f);
+    p.tiles_m = (uint32_t)div_up(g.m, 32u * c.fm);
+    p.tiles_n = (uint32_t)div_up(g.n, 32u * c.fn);
     if (c.splits > 1) {
         p.out = g.workspace;
         p.out_stride = g.n;
@@ -593,9 +656,9 @@ hipError_t launch_gemm(const GemmArgs &g)
         p.out_dtype = kF32;
     }
     const uint32_t blocks = p.tiles_m * p.tiles_n * c.splits;
-    if (c.f == 4) launch_tile<4, BLOCKS, EXACT>(p, blocks, g.stream);
-    else if (c.f == 2) launch_tile<2, BLOCKS, EXACT>(p, blocks, g.stream);
-    else if constexpr (!EXACT) launch_tile<8, BLOCKS, EXACT>(p, blocks, g.stream);
+    if (c.fm == 4) launch_tile<4, 4, BLOCKS, EXACT>(p, blocks, g.stream);
+    else if (c.fm == 2) launch_tile<2, 2, BLOCKS, EXACT>(p, blocks, g.stream);
+    else launch_tile<8, EXACT ? 4 : 8, BLOCKS, EXACT>(p, blocks, g.stream);  // wide operands leave room for half
     if (c.splits > 1) {
         const uint64_t n8 = div_up(g.n, 8), count = g.m * n8;
         const uint64_t wgs = div_up(count, 256);
