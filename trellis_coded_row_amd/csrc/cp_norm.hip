@@ -30,22 +30,60 @@ __device__ __forceinline__ float row_sum(float v, float *part)
     return v;
 }
 
+// 1 / sqrt(v) as a sum hi + lo, lo below hi's last bit: the instruction is off
+// by up to one in the last bit, which a Newton step takes away.
+struct Root {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Root inverse_root(float v)
+{
+    const float r = rsqrtf(v), t = v * r;
+    if (!(r > 0.0f && r < __builtin_inff())) return {r, 0.0f};
+    const float under = fmaf(v, r, -t);              // v r = t + under
+    const float e = fmaf(-t, r, 1.0f) - under * r;   // 1 - v r^2
+    const float step = 0.5f * r * e, hi = r + step;
+    return {hi, step - (hi - r)};
+}
+
+// h * rstd * w rounded once, for values that are rounded to e4m3 next: with
+// each product rounded by itself, more of them change sides at a border
+// between two e4m3 values. Not finite where the plain product is not.
+__device__ __forceinline__ float normed(float h, Root r, float w)
+{
+    const float p = h * r.hi;
+    return fmaf(p, w, fmaf(h, r.lo, fmaf(h, r.hi, -p)) * w);
+}
+
 // The 8-bit outputs of columns [c, c + 8) (y zero past the row's end); the
 // 16 lanes of a row of lanes hold one group of 128.
 __device__ __forceinline__ void put_group(const float *y, uint32_t c, uint32_t d, uint8_t *q, uint8_t *scale)
 {
-    uint32_t m = 0;
+    float most = 0.0f;  // NaN where one of the values is
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t b = finite_bits(y[e]);
-        m = m > b ? m : b;
+    for (int e = 0; e < 8; ++e) most = __builtin_elementwise_maximum(most, __builtin_fabsf(y[e]));
+    uint32_t top = max_of_16(__float_as_uint(most) & 0x7FFFFFFFu);
+    const bool odd = top >= 0x7F800000u;  // the group has values that are not finite
+    if (odd) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = finite_bits(y[e]);
+            m = m > b ? m : b;
+        }
+        top = max_of_16(m);
     }
-    const uint32_t sb = scale_byte(max_of_16(m));
+    const uint32_t sb = scale_byte(top);
     const float inv = inverse_scale(sb);
     if (c >= d) return;
     u32x2 v;
-    v[0] = to_e4m3x4(y[0], y[1], y[2], y[3], inv);
-    v[1] = to_e4m3x4(y[4], y[5], y[6], y[7], inv);
+    if (odd) {
+        v[0] = to_e4m3x4(y[0], y[1], y[2], y[3], inv);
+        v[1] = to_e4m3x4(y[4], y[5], y[6], y[7], inv);
+    } else {
+        v[0] = finite_to_e4m3x4(y[0], y[1], y[2], y[3], inv);
+        v[1] = finite_to_e4m3x4(y[4], y[5], y[6], y[7], inv);
+    }
     if (c + 8 <= d) {
         *reinterpret_cast<u32x2 *>(q + c) = v;
     } else {
@@ -54,53 +92,105 @@ __device__ __forceinline__ void put_group(const float *y, uint32_t c, uint32_t d
     if ((threadIdx.x & 15u) == 0) scale[c >> 7] = (uint8_t)sb;
 }
 
+// Registers that a row's values (x, the residual, the weight) and those of the
+// next row take, per lane; where they are few enough, workgroups stay, keep
+// the weight, and read the next row while they work on this one.
+template <int DT, int IT, bool RES>
+constexpr bool kAhead = (RES ? 5 : 3) * IT * (DT == kF32 ? 8 : 4) <= 40;
+
+constexpr uint32_t kAheadWaves = 4096;  // waves that stay: four for each SIMD unit
+
 // W waves per row, IT chunks of 8 columns per lane: chunk i of a lane is
 // columns 8 (64 W i + lane of the row).
-template <int DT, int W, int IT>
-__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_rows(
+template <int DT, int W, int IT, bool RES>
+__global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_rows(
     const typename Elem<DT>::raw *__restrict__ x, uint64_t x_stride, const typename Elem<DT>::raw *__restrict__ res,
     uint64_t res_stride, const typename Elem<DT>::raw *__restrict__ weight, uint32_t n, uint32_t d, float eps,
     typename Elem<DT>::raw *__restrict__ h_out, typename Elem<DT>::raw *__restrict__ y_out, uint8_t *__restrict__ q,
     uint64_t q_stride, uint8_t *__restrict__ q_scale, uint64_t scale_stride, float *__restrict__ rstd_out)
 {
-    __shared__ float part[W];
-    const uint32_t row = W == 1 ? blockIdx.x * 4u + (threadIdx.x >> 6) : blockIdx.x;
+    typedef typename Elem<DT>::vec8 V;
+    constexpr bool AHEAD = kAhead<DT, IT, RES>;
+    __shared__ float part[2][W];
+    const uint32_t groups = W == 1 ? gridDim.x * 4u : gridDim.x;
+    const uint32_t first = W == 1 ? blockIdx.x * 4u + (threadIdx.x >> 6) : blockIdx.x;
     const uint32_t lane = W == 1 ? threadIdx.x & 63u : threadIdx.x;
-    if (row >= n) return;  // whole waves of a W == 1 workgroup, which has no barrier
-    float h[IT][8];
-    float sum = 0.0f;
-    {
-        typename Elem<DT>::vec8 vx[IT], vr[IT];
+    if (first >= n) return;  // whole waves of a W == 1 workgroup, which has no barrier
+    V vx[IT], vr[RES ? IT : 1], nx[IT], nr[RES ? IT : 1], vw[IT];
+    const auto load = [&](uint32_t row, V *ax, V *ar) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            vx[i] = load8<DT>(x + row * x_stride, (i * W * 64u + lane) * 8u, d);
-            if (res) vr[i] = load8<DT>(res + row * res_stride, (i * W * 64u + lane) * 8u, d);
+            ax[i] = load8<DT>(x + row * x_stride, (i * W * 64u + lane) * 8u, d);
+            if constexpr (RES) ar[i] = load8<DT>(res + row * res_stride, (i * W * 64u + lane) * 8u, d);
         }
+    };
+    const auto value = [&](int i, int e) {
+        float h = Elem<DT>::get(vx[i][e]);
+        if constexpr (RES) h += Elem<DT>::get(vr[i][e]);
+        return h;
+    };
+    load(first, vx, vr);
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) vw[i] = load8<DT>(weight, (i * W * 64u + lane) * 8u, d);
+    }
+    int flip = 0;
+    uint32_t row = first;
+    do {
+        if (AHEAD && row + groups < n) load(row + groups, nx, nr);
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                h[i][e] = Elem<DT>::get(vx[i][e]);
-                if (res) h[i][e] += Elem<DT>::get(vr[i][e]);
-                sum = fmaf(h[i][e], h[i][e], sum);
+                const float h = value(i, e);
+                sum = fmaf(h, h, sum);
             }
         }
-    }
-    sum = row_sum<W>(sum, part);
-    const float rstd = rsqrtf(sum / (float)d + eps);
-    if (rstd_out && lane == 0) rstd_out[row] = rstd;
+        sum = row_sum<W>(sum, part[flip]);  // two places in turn: a barrier a row
+        flip ^= 1;
+        const Root rstd = inverse_root(sum / (float)d + eps);
+        if (rstd_out && lane == 0) rstd_out[row] = rstd.hi;
+        // from here the values are made from x and the residual again: kept,
+        // they would take twice the registers
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const uint32_t c = (i * W * 64u + lane) * 8u;
-        if (h_out && c < d) store8<DT>(h_out + (uint64_t)row * d, c, d, h[i]);
-        if (!y_out && !q) continue;
-        const typename Elem<DT>::vec8 w = load8<DT>(weight, c, d);
-        float y[8];
+        for (int i = 0; i < IT; ++i) {
+            asm volatile("" : "+v"(vx[i]));
+            if constexpr (RES) asm volatile("" : "+v"(vr[i]));
+            if constexpr (AHEAD) asm volatile("" : "+v"(vw[i]));
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = c + e < d ? h[i][e] * rstd * Elem<DT>::get(w[e]) : 0.0f;
-        if (y_out && c < d) store8<DT>(y_out + (uint64_t)row * d, c, d, y);
-        if (q) put_group(y, c, d, q + row * q_stride, q_scale + row * scale_stride);
-    }
+        for (int i = 0; i < IT; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // one chunk's values at a time
+            const uint32_t c = (i * W * 64u + lane) * 8u;
+            if constexpr (RES) {
+                float h[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[e] = value(i, e);
+                if (h_out && c < d) store8<DT>(h_out + (uint64_t)row * d, c, d, h);
+            }
+            if (!AHEAD && (y_out || q)) vw[i] = load8<DT>(weight, c, d);
+            float y[8];
+            if (y_out && c < d) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = value(i, e) * rstd.hi * Elem<DT>::get(vw[i][e]);
+                store8<DT>(y_out + (uint64_t)row * d, c, d, y);
+            }
+            if (q) {  // past the row's end, h and the weight are zero
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = normed(value(i, e), rstd, Elem<DT>::get(vw[i][e]));
+                put_group(y, c, d, q + row * q_stride, q_scale + row * scale_stride);
+            }
+        }
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                vx[i] = nx[i];
+                if constexpr (RES) vr[i] = nr[i];
+            }
+        }
+        row += groups;
+    } while (AHEAD && row < n);
 }
 
 // Rows too long for registers: the row is read twice.
@@ -116,7 +206,7 @@ __global__ __launch_bounds__(kLongWaves * 64) void norm_long(
     __shared__ float part[kLongWaves];
     const uint64_t row = blockIdx.x;
     const uint32_t step = kLongWaves * 64u * 8u;
-    float rstd = 0.0f;
+    Root rstd{};
     for (int pass = 0; pass < 2; ++pass) {
         float sum = 0.0f;
         for (uint32_t c0 = 0; c0 < d; c0 += step) {  // all lanes, for put_group's maximum
@@ -137,47 +227,62 @@ __global__ __launch_bounds__(kLongWaves * 64) void norm_long(
                 if (h_out && c < d) store8<DT>(h_out + row * d, c, d, h);
                 const typename Elem<DT>::vec8 w = load8<DT>(weight, c, d);
                 float y[8];
+                if (y_out && c < d) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = c + e < d ? h[e] * rstd * Elem<DT>::get(w[e]) : 0.0f;
-                if (y_out && c < d) store8<DT>(y_out + row * d, c, d, y);
-                if (q) put_group(y, c, d, q + row * q_stride, q_scale + row * scale_stride);
+                    for (int e = 0; e < 8; ++e) y[e] = h[e] * rstd.hi * Elem<DT>::get(w[e]);
+                    store8<DT>(y_out + row * d, c, d, y);
+                }
+                if (q) {  // past the row's end, h and the weight are zero
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = normed(h[e], rstd, Elem<DT>::get(w[e]));
+                    put_group(y, c, d, q + row * q_stride, q_scale + row * scale_stride);
+                }
             }
         }
         if (pass == 0) {
             sum = row_sum<kLongWaves>(sum, part);
-            rstd = rsqrtf(sum / (float)d + eps);
-            if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
+            rstd = inverse_root(sum / (float)d + eps);
+            if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd.hi;
         }
     }
 }
 
-template <int DT, int W, int IT>
+template <int DT, int W, int IT, bool RES>
 void norm_launch(const NormArgs &a)
 {
     typedef typename Elem<DT>::raw R;
-    norm_rows<DT, W, IT><<<(uint32_t)(W == 1 ? div_up(a.n, 4) : a.n), W == 1 ? 256 : W * 64, 0, a.stream>>>(
+    uint64_t blocks = W == 1 ? div_up(a.n, 4) : a.n;
+    const uint64_t stay = kAheadWaves / (W == 1 ? 4 : W);
+    if (kAhead<DT, IT, RES> && blocks > stay) blocks = stay;
+    norm_rows<DT, W, IT, RES><<<(uint32_t)blocks, W == 1 ? 256 : W * 64, 0, a.stream>>>(
         (const R *)a.x, a.x_stride, (const R *)a.residual, a.residual_stride, (const R *)a.weight, (uint32_t)a.n,
         (uint32_t)a.d, a.eps, (R *)a.h, (R *)a.y, a.q, a.q_stride, a.q_scale, a.scale_stride, a.rstd);
 }
 
-template <int DT>
+template <int DT, bool RES>
 hipError_t norm_of(const NormArgs &a)
 {
     typedef typename Elem<DT>::raw R;
     const bool few = a.n <= 512;  // rows for two workgroups per compute unit at most: more waves per row
-    if (a.d <= 512) norm_launch<DT, 1, 1>(a);
-    else if (a.d <= 1024) norm_launch<DT, 1, 2>(a);
-    else if (a.d <= 2048) norm_launch<DT, 4, 1>(a);
-    else if (a.d <= 4096) few ? norm_launch<DT, 8, 1>(a) : norm_launch<DT, 4, 2>(a);
-    else if (a.d <= 8192) few ? norm_launch<DT, 16, 1>(a) : norm_launch<DT, 8, 2>(a);
-    else if (a.d <= 16384) norm_launch<DT, 16, 2>(a);
-    else if (a.d <= 24576) norm_launch<DT, 16, 3>(a);
-    else if (a.d <= 32768) norm_launch<DT, 16, 4>(a);
+    if (a.d <= 512) norm_launch<DT, 1, 1, RES>(a);
+    else if (a.d <= 1024) norm_launch<DT, 1, 2, RES>(a);
+    else if (a.d <= 2048) norm_launch<DT, 4, 1, RES>(a);
+    else if (a.d <= 4096) few ? norm_launch<DT, 8, 1, RES>(a) : norm_launch<DT, 4, 2, RES>(a);
+    else if (a.d <= 8192) few ? norm_launch<DT, 16, 1, RES>(a) : norm_launch<DT, 8, 2, RES>(a);
+    else if (a.d <= 16384) norm_launch<DT, 16, 2, RES>(a);
+    else if (a.d <= 24576) norm_launch<DT, 16, 3, RES>(a);
+    else if (a.d <= 32768) norm_launch<DT, 16, 4, RES>(a);
     else
         norm_long<DT><<<(uint32_t)a.n, kLongWaves * 64, 0, a.stream>>>(
             (const R *)a.x, a.x_stride, (const R *)a.residual, a.residual_stride, (const R *)a.weight, (uint32_t)a.d,
             a.eps, (R *)a.h, (R *)a.y, a.q, a.q_stride, a.q_scale, a.scale_stride, a.rstd);
     return hipGetLastError();
+}
+
+template <int DT>
+hipError_t norm_type(const NormArgs &a)
+{
+    return a.residual ? norm_of<DT, true>(a) : norm_of<DT, false>(a);
 }
 
 // -------------------------------------------------------------- gradient
@@ -399,7 +504,9 @@ hipError_t rms_norm(const NormArgs &args)
     const uint64_t es = dtype_bytes(a.dtype);
     for (uint64_t left = args.n; left > 0;) {  // a launch has fewer than 2^32 threads
         a.n = left < kMaxRows ? left : kMaxRows;
-        const hipError_t e = a.dtype == kF32 ? norm_of<kF32>(a) : a.dtype == kBF16 ? norm_of<kBF16>(a) : norm_of<kF16>(a);
+        const hipError_t e = a.dtype == kF32    ? norm_type<kF32>(a)
+                             : a.dtype == kBF16 ? norm_type<kBF16>(a)
+                                                : norm_type<kF16>(a);
         if (e != hipSuccess) return e;
         left -= a.n;
         a.x = (const uint8_t *)a.x + a.n * a.x_stride * es;

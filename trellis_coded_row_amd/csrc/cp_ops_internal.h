@@ -217,6 +217,14 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
     return (uint32_t)r;
 }
 
+// The same for finite values.
+__device__ __forceinline__ uint32_t finite_to_e4m3x4(float a, float b, float c, float d, float inv)
+{
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, r, true);
+    return (uint32_t)r;
+}
+
 // The value of the lane r places further round this lane's row of 16.
 template <int R>
 __device__ __forceinline__ int row_rotate(int v)
