@@ -475,12 +475,15 @@ __global__ __launch_bounds__(256) void join_splits(const float *__restrict__ par
 
 // Few rows of A (16 MT at most): B is read once and bounds the time. A
 // workgroup has 16 columns of the output; its W waves take runs of steps of
-// k, four steps' loads in flight, straight into registers, and add their
-// sums through LDS.
-template <int MT, int W, bool BLOCKS, bool EXACT>
-__global__ __launch_bounds__(W * 64) void gemm_rows(TileParams p)
+// k, straight into registers, and add their sums through LDS. A wave reads
+// the next U steps while it multiplies U: 8 KiB of B in flight for each of
+// a compute unit's eight waves. (A comes from L2; with 64 rows of it there
+// is room for one U of them only.)
+template <int MT, int W, bool BLOCKS, bool EXACT, bool KTAIL>
+__global__ __launch_bounds__(W * 64, 2) void gemm_rows(TileParams p)
 {
-    constexpr int U = MT <= 2 ? 4 : 2;  // steps in flight
+    constexpr int U = 4;  // steps read together: those of a dword of scales
+    constexpr bool A_AHEAD = MT <= 2;
     __shared__ f32x4 sums[W][MT][64];
     const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t r = lane & 15u, g = lane >> 4;
@@ -488,7 +491,7 @@ __global__ __launch_bounds__(W * 64) void gemm_rows(TileParams p)
     const uint32_t steps = (p.k + kStep - 1) / kStep;
     const uint32_t s0 = w * p.steps_per_split < steps ? w * p.steps_per_split : steps;
     const uint32_t s1 = s0 + p.steps_per_split < steps ? s0 + p.steps_per_split : steps;
-    const auto ra = buffer_of(p.a), rb = buffer_of(p.b + (uint64_t)n0 * p.b_stride);
+    const uint8_t *const pb = p.b + (uint64_t)n0 * p.b_stride;
     const uint32_t nr = n0 + r < p.n ? r : p.n - 1 - n0;
     const uint32_t vb = nr * p.b_stride + g * 16;
     uint32_t va[MT];
@@ -506,41 +509,73 @@ __global__ __launch_bounds__(W * 64) void gemm_rows(TileParams p)
     // 16 bytes at k of a row whose first byte this lane reads at offset v
     const auto load = [&](__amdgpu_buffer_rsrc_t rsrc, uint32_t v, uint32_t k0, uint32_t half) {
         const uint32_t k = k0 + half * 64 + g * 16;
-        i32x4 x = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                rsrc, k < p.k ? v + half * 64 : kOutside, k0, 0));
-        if (k < p.k && k + 16 > p.k) {  // bytes past k may hold anything
-            const uint32_t keep = p.k - k;
+        const uint32_t at = KTAIL && k >= p.k ? kOutside : v + half * 64;
+        return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, k0, 0));
+    };
+    // bytes past k may hold anything
+    const auto trim = [&](i32x8 x, uint32_t k0) {
+        if constexpr (KTAIL) {
 #pragma unroll
-            for (uint32_t q = 0; q < 4; ++q) {
-                const uint32_t kq = keep > 4 * q ? keep - 4 * q : 0;
-                if (kq < 4) x[q] &= (int)((1u << (8 * kq)) - 1u);
+            for (uint32_t q = 0; q < 8; ++q) {
+                const uint32_t k = k0 + (q / 4) * 64 + g * 16 + (q % 4) * 4;
+                if (k + 4 > p.k) x[q] &= k < p.k ? (int)((1u << (8 * (p.k - k))) - 1u) : 0;
             }
         }
         return x;
     };
-    for (uint32_t s = s0; s < s1; s += U) {
-        int sa[MT], sb = *reinterpret_cast<const int *>(psb + (s & ~3u));
-#pragma unroll
-        for (int t = 0; t < MT; ++t) sa[t] = *reinterpret_cast<const int *>(psa[t] + (s & ~3u));
+    struct Batch {
         i32x8 b[U], a[U][MT];
+        int sb, sa[MT];
+    };
+    const auto load_a = [&](uint32_t s, Batch &x) {
+        const uint32_t at = s < s1 ? s : 0;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) x.sa[t] = *reinterpret_cast<const int *>(psa[t] + at);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t k0 = (s + u) * kStep;  // past the last step: zeros or a neighbour's, not multiplied
-            b[u] = join(load(rb, vb, k0, 0), load(rb, vb, k0, 1));
+            const auto ra = buffer_of(p.a, s + u < s1 ? kInside : 0);
 #pragma unroll
-            for (int t = 0; t < MT; ++t) a[u][t] = join(load(ra, va[t], k0, 0), load(ra, va[t], k0, 1));
+            for (int t = 0; t < MT; ++t)
+                x.a[u][t] = join(load(ra, va[t], (s + u) * kStep, 0), load(ra, va[t], (s + u) * kStep, 1));
         }
+    };
+    const auto load_b = [&](uint32_t s, Batch &x) {
+        x.sb = *reinterpret_cast<const int *>(psb + (s < s1 ? s : 0));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const auto rb = buffer_of(pb, s + u < s1 ? kInside : 0);  // past the wave's last step: nothing is read
+            x.b[u] = join(load(rb, vb, (s + u) * kStep, 0), load(rb, vb, (s + u) * kStep, 1));
+        }
+    };
+    const auto multiply = [&](uint32_t s, Batch &x) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s + u >= s1) break;
-            const uint32_t sh = 8 * ((s + u) & 3u);
+            const i32x8 b = trim(x.b[u], (s + u) * kStep);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
+                const i32x8 a = trim(x.a[u][t], (s + u) * kStep);
                 if constexpr (EXACT)
-                    acc[t] = mfma_wide(widen(b[u], scale_of<0>(sb >> sh)), widen(a[u][t], scale_of<0>(sa[t] >> sh)), acc[t]);
-                else acc[t] = mfma<0>(b[u], a[u][t], acc[t], sb >> sh, sa[t] >> sh);
+                    acc[t] = mfma_wide(widen(b, scale_of<0>(x.sb >> (8 * u))), widen(a, scale_of<0>(x.sa[t] >> (8 * u))),
+                                       acc[t]);
+                else acc[t] = mfma<0>(b, a, acc[t], x.sb >> (8 * u), x.sa[t] >> (8 * u));
             }
         }
+    };
+    Batch x, y;
+    const auto turn = [&](uint32_t s, Batch &now, Batch &next) {
+        load_b(s + U, next);
+        if constexpr (A_AHEAD) load_a(s + U, next);
+        else load_a(s, now);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s, now);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    load_b(s0, x);
+    if constexpr (A_AHEAD) load_a(s0, x);
+    for (uint32_t s = s0; s < s1; s += 2 * U) {
+        turn(s, x, y);
+        turn(s + U, y, x);
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t) sums[w][t][lane] = acc[t];
@@ -560,6 +595,8 @@ __global__ __launch_bounds__(W * 64) void gemm_rows(TileParams p)
     }
 }
 
+constexpr int kRowWaves = 8;
+
 // How a product is cut: the rows kernel, or tiles of 32 f x 32 f and splits
 // of k.
 struct Cut {
@@ -575,8 +612,7 @@ Cut cut_of(uint64_t m, uint64_t n, uint64_t k, bool exact)
     if (m <= 64) {
         best.rows = m <= 16 ? 1 : m <= 32 ? 2 : 4;
         best.splits = 1;
-        const uint32_t waves = best.rows == 1 ? 16 : 8;
-        best.steps_per_split = (uint32_t)(div_up(div_up(steps, waves), 4) * 4);  // scales are read four steps at a time
+        best.steps_per_split = (uint32_t)(div_up(div_up(steps, kRowWaves), 4) * 4);  // scales are read four steps at a time
         return best;
     }
     // time of each cut in cycles of one compute unit: rounds of workgroups
@@ -620,6 +656,13 @@ void launch_tile(const TileParams &p, uint32_t blocks, hipStream_t stream)
     else gemm_tile<FM, FN, BLOCKS, false, EXACT><<<blocks, 256, 0, stream>>>(p);
 }
 
+template <int MT, bool BLOCKS, bool EXACT>
+void launch_rows(const TileParams &p, uint32_t blocks, hipStream_t stream)
+{
+    if (p.k % kStep) gemm_rows<MT, kRowWaves, BLOCKS, EXACT, true><<<blocks, kRowWaves * 64, 0, stream>>>(p);
+    else gemm_rows<MT, kRowWaves, BLOCKS, EXACT, false><<<blocks, kRowWaves * 64, 0, stream>>>(p);
+}
+
 template <bool BLOCKS, bool EXACT>
 hipError_t launch_gemm(const GemmArgs &g)
 {
@@ -642,9 +685,9 @@ hipError_t launch_gemm(const GemmArgs &g)
     p.out_dtype = g.out_dtype;
     if (c.rows) {
         const uint32_t blocks = (uint32_t)div_up(g.n, 16);
-        if (c.rows == 1) gemm_rows<1, 16, BLOCKS, EXACT><<<blocks, 1024, 0, g.stream>>>(p);
-        else if (c.rows == 2) gemm_rows<2, 8, BLOCKS, EXACT><<<blocks, 512, 0, g.stream>>>(p);
-        else gemm_rows<4, 8, BLOCKS, EXACT><<<blocks, 512, 0, g.stream>>>(p);
+        if (c.rows == 1) launch_rows<1, BLOCKS, EXACT>(p, blocks, g.stream);
+        else if (c.rows == 2) launch_rows<2, BLOCKS, EXACT>(p, blocks, g.stream);
+        else launch_rows<4, BLOCKS, EXACT>(p, blocks, g.stream);
         return hipGetLastError();
     }
     p.tiles_m = (uint32_t)div_up(g.m, 32u * c.fm);
