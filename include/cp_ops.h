@@ -71,7 +71,7 @@ uint64_t cp_embed_plan_workspace_bytes(uint64_t n, uint64_t rows);
  *   order  - device int32[n] (written: the first starts[*count]): positions
  *            in the batch, by row, then by position.
  *   slot   - device int32[n]: slot[i] = the distinct row that order[i] looked
- *            up, as its index in unique.
+ *            up, as its index in unique; -1 from starts[*count] on.
  *   unique - device int64[n]: the distinct rows, ascending.
  *   starts - device int32[n + 1]: row unique[u]'s lookups are
  *            order[starts[u] .. starts[u + 1]).
@@ -94,7 +94,8 @@ uint64_t cp_embed_grad_workspace_bytes(uint64_t n, uint64_t d);
  *   dout      - device, n x d of dtype, dout_stride elements apart.
  *   workspace - device, 256-byte aligned, >= cp_embed_grad_workspace_bytes.
  * Errors: INVALID_ARGUMENT (NULL or misaligned pointers, unknown dtype,
- * n or d above 2^31 - 4096, workspace too small), HIP. */
+ * n or d above 2^31 - 4096, workspace too small), UNSUPPORTED (d above 2^21),
+ * HIP. */
 cp_status cp_embed_grad(const int32_t *order, const int32_t *slot, const int64_t *unique, const int32_t *starts,
                         const int64_t *count, uint64_t n, uint64_t rows, const void *dout, cp_dtype dtype, uint64_t d,
                         uint64_t dout_stride, float scale, float *grad, void *workspace, uint64_t workspace_bytes,

@@ -13,7 +13,9 @@ namespace cpk {
 
 namespace {
 
-constexpr uint32_t kMaxBlocks = 1u << 22;  // workgroups of one launch, at most
+// What a kernel only reads: from here the compiler may use scalar loads.
+typedef const __attribute__((address_space(4))) int32_t *const_i32;
+typedef const __attribute__((address_space(4))) int64_t *const_i64;
 
 // Lanes that share a row of d elements, 8 elements each: a power of two.
 int row_lanes_log2(uint64_t d)
@@ -25,46 +27,74 @@ int row_lanes_log2(uint64_t d)
 
 // ---------------------------------------------------------------- lookup
 
-// 2^gs lanes take a row, 8 elements each per step; a thread has U rows'
-// loads in flight.
-template <int TI, int TO, int U>
+// 2^gs lanes take a row, 8 elements each; blockIdx.y + slice0: a slice of
+// 8 << gs columns. Workgroup b takes groups of U (256 >> gs) rows: the b-th, the one
+// gridDim.x further, and so on. Where a batch has more groups than the chip
+// holds workgroups, a group's rows are read while the one before is written,
+// and its ids before that. WAVE: gs is 6, so that the ids are the same in
+// all of a wave's lanes and go through scalar registers and loads.
+template <int TI, int TO, int U, bool WAVE>
 __global__ __launch_bounds__(256) void lookup_rows(const typename Elem<TI>::raw *__restrict__ table, uint64_t rows,
-                                                   uint32_t d, uint64_t stride, const int64_t *__restrict__ ids,
+                                                   uint32_t d, uint64_t stride, const_i64 ids,
                                                    uint32_t n, float scale, typename Elem<TO>::raw *__restrict__ out,
-                                                   int32_t *__restrict__ bad_id, int gs)
+                                                   int32_t *__restrict__ bad_id, int gs, uint32_t slice0)
 {
-    const uint32_t lane = threadIdx.x & ((1u << gs) - 1u);
+    typedef typename Elem<TI>::vec8 V;
+    if constexpr (WAVE) gs = 6;
     const uint32_t per = 256u >> gs;
-    const uint64_t j0 = (uint64_t)blockIdx.x * (U * per) + (threadIdx.x >> gs);
-    int64_t id[U];
+    const uint32_t c = (((slice0 + blockIdx.y) << gs) + (threadIdx.x & ((1u << gs) - 1u))) * 8u;
+    const uint32_t step = gridDim.x * U * per;  // below 2^22, and n below 2^31
+    uint32_t j = blockIdx.x * (U * per) + (threadIdx.x >> gs);
+    if constexpr (WAVE) j = __builtin_amdgcn_readfirstlane(j);
+    if (c >= d) return;
+    int64_t id[U], after[U];
+    V v[U];
+    const auto read_ids = [&](uint32_t at, int64_t *to) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) id[u] = j0 + u * per < n ? ids[j0 + u * per] : -1;
-    bool bad = false;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (id[u] >= 0 && (uint64_t)id[u] >= rows) {
-            bad = true;
-            id[u] = -1;
-        }
-    }
-    if (bad && bad_id) *bad_id = 1;
-    for (uint32_t c = lane * 8u; c < d; c += 8u << gs) {
-        typename Elem<TI>::vec8 v[U];
+        for (int u = 0; u < U; ++u) to[u] = at + u * per < n ? ids[at + u * per] : -1;
+    };
+    const auto read_rows = [&](int64_t *of, V *to) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (id[u] >= 0) v[u] = load8<TI>(table + (uint64_t)id[u] * stride, c, d);
-            else v[u] = (typename Elem<TI>::raw)0;
+            if (of[u] >= 0 && (uint64_t)of[u] >= rows) {
+                of[u] = -1;
+                if (bad_id) *bad_id = 1;
+            }
+            if (of[u] >= 0) to[u] = load8<TI>(table + (uint64_t)of[u] * stride, c, d);
+            else to[u] = (typename Elem<TI>::raw)0;
+        }
+    };
+    read_ids(j, id);
+    read_rows(id, v);
+    read_ids(j + step, after);
+    while (j < n) {
+        V next[U];
+        bool none[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) none[u] = id[u] < 0;
+        if (j + step < n) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) id[u] = after[u];
+            read_rows(id, next);
+            read_ids(j + 2 * step, after);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (j0 + u * per >= n) continue;
+            if (j + u * per >= n) continue;
             float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = id[u] >= 0 ? Elem<TI>::get(v[u][e]) * scale : 0.0f;
-            store8<TO, true>(out + (j0 + u * per) * d, c, d, f);
+            for (int e = 0; e < 8; ++e) f[e] = none[u] ? 0.0f : Elem<TI>::get(v[u][e]) * scale;  // padding: +0 for any scale
+            store8<TO, true>(out + (uint64_t)(j + u * per) * d, c, d, f);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = next[u];
+        j += step;
     }
 }
+
+// Workgroups that stay: as many as the registers let each compute unit hold.
+constexpr uint32_t kLookupBlocksWave = 256 * 8, kLookupBlocks = 256 * 4;
+constexpr uint32_t kLookupSlices = 4096;  // slices of one launch, at most (it has fewer than 2^32 threads)
 
 template <int TI, int TO>
 hipError_t launch_lookup(const EmbedLookupArgs &a)
@@ -72,20 +102,20 @@ hipError_t launch_lookup(const EmbedLookupArgs &a)
     typedef typename Elem<TI>::raw RI;
     typedef typename Elem<TO>::raw RO;
     const int gs = row_lanes_log2(a.d);
-    const uint32_t per = 256u >> gs;
-    // four rows in flight per thread once that still leaves the chip several
-    // workgroups per compute unit
-    const bool four = a.n >= 4ull * per * 2048;
-    const uint64_t step = (uint64_t)kMaxBlocks * per * (four ? 4 : 1);
-    for (uint64_t j = 0; j < a.n; j += step) {  // a launch has fewer than 2^32 threads
-        const uint32_t n = (uint32_t)(a.n - j < step ? a.n - j : step);
-        RO *out = (RO *)a.out + j * a.d;
-        if (four)
-            lookup_rows<TI, TO, 4><<<(uint32_t)div_up(n, 4ull * per), 256, 0, a.stream>>>(
-                (const RI *)a.table, a.rows, (uint32_t)a.d, a.row_stride, a.ids + j, n, a.scale, out, a.bad_id, gs);
-        else
-            lookup_rows<TI, TO, 1><<<(uint32_t)div_up(n, per), 256, 0, a.stream>>>(
-                (const RI *)a.table, a.rows, (uint32_t)a.d, a.row_stride, a.ids + j, n, a.scale, out, a.bad_id, gs);
+    const uint32_t per = 256u >> gs, slices = (uint32_t)div_up(a.d, 8ull << gs);
+    // four rows in flight per thread once that still fills the chip
+    const uint32_t most = gs == 6 ? kLookupBlocksWave : kLookupBlocks;
+    const bool four = a.n >= 4ull * per * most;
+    const uint64_t groups = div_up(a.n, (four ? 4ull : 1ull) * per);
+    const uint32_t blocks = (uint32_t)(groups < most ? groups : most);
+    for (uint32_t y = 0; y < slices; y += kLookupSlices) {
+        const dim3 grid(blocks, slices - y < kLookupSlices ? slices - y : kLookupSlices);
+        const auto launch = [&](auto kernel) {
+            kernel<<<grid, 256, 0, a.stream>>>((const RI *)a.table, a.rows, (uint32_t)a.d, a.row_stride,
+                                               (const_i64)a.ids, (uint32_t)a.n, a.scale, (RO *)a.out, a.bad_id, gs, y);
+        };
+        if (gs == 6) four ? launch(lookup_rows<TI, TO, 4, true>) : launch(lookup_rows<TI, TO, 1, true>);
+        else four ? launch(lookup_rows<TI, TO, 4, false>) : launch(lookup_rows<TI, TO, 1, false>);
     }
     return hipGetLastError();
 }
@@ -145,8 +175,21 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *wave_sum,
     return before + v;
 }
 
-// hist[digit][tile] = keys of the tile with that digit.
-template <typename K, bool FIRST>
+// Where the count of a tile's keys with a digit stands: for few tiles, by
+// tile (a scatter adds up the earlier tiles' counts by itself, a launch
+// less); else by digit (sort_scan adds them up). The threshold keeps those
+// loads in flight together.
+constexpr uint32_t kDirectTiles = 32;
+
+template <bool DIRECT>
+__device__ __forceinline__ uint64_t count_at(uint32_t tile, uint32_t digit, uint32_t ntiles, uint32_t digits)
+{
+    return DIRECT ? (uint64_t)tile * digits + digit : (uint64_t)digit * ntiles + tile;
+}
+
+// (Counting a pass's keys where the pass before puts them, by atomics, was
+// slower than this launch: 25 to 50 us, as frequent rows' keys meet.)
+template <typename K, bool FIRST, bool DIRECT>
 __global__ __launch_bounds__(kSortThreads) void sort_count(const int64_t *__restrict__ ids, uint64_t rows,
                                                            const K *__restrict__ keys, uint32_t n, int shift,
                                                            uint32_t digits, uint32_t ntiles,
@@ -167,7 +210,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count(const int64_t *__rest
         }
     }
     __syncthreads();
-    if (threadIdx.x < digits) hist[(uint64_t)threadIdx.x * ntiles + blockIdx.x] = cnt[threadIdx.x];
+    if (threadIdx.x < digits) hist[count_at<DIRECT>(blockIdx.x, threadIdx.x, ntiles, digits)] = cnt[threadIdx.x];
 }
 
 // Per digit: hist[digit][tile] becomes the count of the tiles before it,
@@ -192,7 +235,7 @@ __global__ __launch_bounds__(256) void sort_scan(uint32_t *__restrict__ hist, ui
 // Each key to its place: the keys of smaller digits, the same digit's in
 // earlier tiles, in earlier waves' parts of this tile, and in this wave
 // before it. Wave w has keys [w, w + 1) * 64 * kSortRounds of the tile.
-template <typename K, bool FIRST>
+template <typename K, bool FIRST, bool DIRECT>
 __global__ __launch_bounds__(kSortThreads) void sort_scatter(const int64_t *__restrict__ ids, uint64_t rows,
                                                              const K *__restrict__ keys,
                                                              const int32_t *__restrict__ vals, uint32_t n, int shift,
@@ -227,8 +270,22 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter(const int64_t *__re
     }
     uint32_t before = 0, total = 0;
     if (threadIdx.x < digits) {
-        before = hist[(uint64_t)threadIdx.x * ntiles + blockIdx.x];
-        total = totals[threadIdx.x];
+        if constexpr (DIRECT) {
+            constexpr uint32_t B = 8;  // loads in flight
+            for (uint32_t t0 = 0; t0 < ntiles; t0 += B) {
+                uint32_t c[B];
+#pragma unroll
+                for (uint32_t q = 0; q < B; ++q) c[q] = t0 + q < ntiles ? hist[(t0 + q) * digits + threadIdx.x] : 0;
+#pragma unroll
+                for (uint32_t q = 0; q < B; ++q) {
+                    total += c[q];
+                    before += t0 + q < blockIdx.x ? c[q] : 0;
+                }
+            }
+        } else {
+            before = hist[(uint64_t)threadIdx.x * ntiles + blockIdx.x];
+            total = totals[threadIdx.x];
+        }
     }
     uint32_t all;
     before += block_prefix<kSortWaves>(total, wave_sum, &all) - total;  // holds the barrier for cnt too
@@ -307,7 +364,7 @@ __global__ __launch_bounds__(kSortThreads) void write_runs(const K *__restrict__
         const bool head = valid && (i == 0 || keys[i - 1] != k);
         const uint32_t u = base + block_prefix<kSortWaves>(head ? 1u : 0u, wave_sum, &all) - 1u;
         base += all;
-        if (valid) slot[i] = (int32_t)u;
+        if (in) slot[i] = valid ? (int32_t)u : -1;
         if (head) {
             unique[u] = (int64_t)k;
             starts[u] = (int32_t)i;
@@ -354,13 +411,25 @@ PlanLayout plan_layout(uint64_t n, uint64_t rows)
     return L;
 }
 
+template <typename K, bool FIRST, bool DIRECT>
+void launch_pass(const EmbedPlanArgs &a, const PlanLayout &L, const K *keys, const int32_t *vals, int shift, int bits,
+                 K *keys_out, int32_t *vals_out)
+{
+    const uint32_t n = (uint32_t)a.n, ntiles = (uint32_t)div_up(a.n, kSortTile);
+    uint32_t *const hist = reinterpret_cast<uint32_t *>(a.workspace + L.hist);
+    uint32_t *const totals = reinterpret_cast<uint32_t *>(a.workspace + L.totals);
+    sort_count<K, FIRST, DIRECT><<<ntiles, kSortThreads, 0, a.stream>>>(a.ids, a.rows, keys, n, shift, 1u << bits,
+                                                                        ntiles, hist);
+    if constexpr (!DIRECT) sort_scan<<<1u << bits, 256, 0, a.stream>>>(hist, ntiles, totals);
+    sort_scatter<K, FIRST, DIRECT><<<ntiles, kSortThreads, 0, a.stream>>>(a.ids, a.rows, keys, vals, n, shift, bits,
+                                                                          ntiles, hist, totals, keys_out, vals_out);
+}
+
 template <typename K>
 hipError_t launch_plan(const EmbedPlanArgs &a)
 {
     const PlanLayout L = plan_layout(a.n, a.rows);
     const uint32_t n = (uint32_t)a.n, ntiles = (uint32_t)div_up(a.n, kSortTile);
-    uint32_t *const hist = reinterpret_cast<uint32_t *>(a.workspace + L.hist);
-    uint32_t *const totals = reinterpret_cast<uint32_t *>(a.workspace + L.totals);
     uint32_t *const heads = reinterpret_cast<uint32_t *>(a.workspace + L.heads);
     K *keys[2] = {reinterpret_cast<K *>(a.workspace + L.keys0), reinterpret_cast<K *>(a.workspace + L.keys1)};
     int32_t *vals[2] = {reinterpret_cast<int32_t *>(a.workspace + L.vals0),
@@ -369,23 +438,18 @@ hipError_t launch_plan(const EmbedPlanArgs &a)
     while (key_bits < 64 && (a.rows >> key_bits) != 0) ++key_bits;
     const int passes = (key_bits + kDigitBits - 1) / kDigitBits;
     const int bits = (key_bits + passes - 1) / passes;
+    const bool direct = ntiles <= kDirectTiles;
     for (int p = 0; p < passes; ++p) {
-        const int shift = p * bits;
         const K *in = keys[(p + 1) & 1];
         K *out = keys[p & 1];
+        const int32_t *vin = vals[(p + 1) & 1];
         int32_t *vout = p + 1 == passes ? a.order : vals[p & 1];
         if (p == 0) {
-            sort_count<K, true><<<ntiles, kSortThreads, 0, a.stream>>>(a.ids, a.rows, nullptr, n, shift, 1u << bits,
-                                                                       ntiles, hist);
-            sort_scan<<<1u << bits, 256, 0, a.stream>>>(hist, ntiles, totals);
-            sort_scatter<K, true><<<ntiles, kSortThreads, 0, a.stream>>>(a.ids, a.rows, nullptr, nullptr, n, shift,
-                                                                         bits, ntiles, hist, totals, out, vout);
+            if (direct) launch_pass<K, true, true>(a, L, nullptr, nullptr, 0, bits, out, vout);
+            else launch_pass<K, true, false>(a, L, nullptr, nullptr, 0, bits, out, vout);
         } else {
-            sort_count<K, false><<<ntiles, kSortThreads, 0, a.stream>>>(nullptr, a.rows, in, n, shift, 1u << bits,
-                                                                        ntiles, hist);
-            sort_scan<<<1u << bits, 256, 0, a.stream>>>(hist, ntiles, totals);
-            sort_scatter<K, false><<<ntiles, kSortThreads, 0, a.stream>>>(nullptr, a.rows, in, vals[(p + 1) & 1], n,
-                                                                          shift, bits, ntiles, hist, totals, out, vout);
+            if (direct) launch_pass<K, false, true>(a, L, in, vin, p * bits, bits, out, vout);
+            else launch_pass<K, false, false>(a, L, in, vin, p * bits, bits, out, vout);
         }
     }
     const K *sorted = keys[(passes - 1) & 1];
@@ -396,53 +460,73 @@ hipError_t launch_plan(const EmbedPlanArgs &a)
 
 // -------------------------------------------------------------- gradient
 
-// Sorted lookups per chunk: a chunk is summed by one group of lanes.
+// Sorted lookups per chunk: a chunk is summed by one group of lanes. Few, so
+// that no group's rows, read a few at a time, outlast the others'.
 uint32_t grad_chunk(uint64_t n)
 {
     uint32_t c = 8;
-    while (c < 64 && n / c > 4096) c <<= 1;
+    while ((c < 32 && n / c > 4096) || n / c > (1u << 24)) c <<= 1;  // (a launch has fewer than 2^32 threads)
     return c;
 }
 
-// A row with more than kLongChunks chunks' worth of lookups is summed by
-// chunks (partial sums, joined afterwards); any other by the chunk in which
-// its run begins.
-constexpr uint32_t kLongChunks = 4;
+// A row with more lookups than a chunk (a long run) is summed by chunks
+// (partial sums, joined afterwards); any other by the chunk in which its run
+// begins.
 
 // Row s's sum goes to grad row `rows ? unique[s] : s`.
-__device__ __forceinline__ float *grad_row(float *grad, const int64_t *unique, uint64_t rows, int32_t s, uint64_t d)
+template <typename P>
+__device__ __forceinline__ float *grad_row(float *grad, P unique, uint64_t rows, int32_t s, uint64_t d)
 {
     return grad + (rows ? (uint64_t)unique[s] : (uint64_t)(uint32_t)s) * d;
 }
 
+struct GradParams {
+    const_i32 order, slot;
+    const_i64 unique;
+    const_i32 starts;
+    const_i64 count;
+    uint64_t rows;
+    const void *dout;
+    uint32_t n, d;
+    uint64_t stride;
+    float scale;
+    float *grad, *partial;
+    uint32_t C;       // lookups per chunk
+    int gs;           // 2^gs lanes per chunk
+    uint32_t blocks;  // workgroups along x that sum chunks; those after it clear rows
+    uint32_t zero_rows;
+};
+
 // Chunk c: sorted lookups [c C, c C + C). Its group of 2^gs lanes sums the
 // runs that begin in it, reading past its end for a short last run, and its
 // own part of a long run into partial[2 c] (begun in an earlier chunk) or
-// partial[2 c + 1] (begun in this one). blockIdx.y: a slice of 8 << gs columns.
-template <int DT>
-__global__ __launch_bounds__(256) void grad_chunks(const int32_t *__restrict__ order, const int32_t *__restrict__ slot,
-                                                   const int64_t *__restrict__ unique,
-                                                   const int32_t *__restrict__ starts,
-                                                   const int64_t *__restrict__ count, uint64_t rows,
-                                                   const typename Elem<DT>::raw *__restrict__ dout, uint32_t d,
-                                                   uint64_t stride, float scale, float *__restrict__ grad,
-                                                   float *__restrict__ partial, uint32_t C, int gs)
+// partial[2 c + 1] (begun in this one). blockIdx.y: a slice of 8 << gs
+// columns. WAVE: gs is 6, so that everything but the row's values is the same
+// in all of a wave's lanes and goes through scalar registers and loads.
+template <int DT, bool WAVE>
+__device__ __forceinline__ void grad_chunk_sum(const GradParams &p)
 {
     constexpr int U = 8;  // rows' loads in flight
+    const int gs = WAVE ? 6 : p.gs;
+    const uint32_t d = p.d, C = p.C;
     const uint32_t lane = threadIdx.x & ((1u << gs) - 1u);
-    const uint32_t chunk = blockIdx.x * (256u >> gs) + (threadIdx.x >> gs);
+    uint32_t chunk = blockIdx.x * (256u >> gs) + (threadIdx.x >> gs);
+    if constexpr (WAVE) chunk = __builtin_amdgcn_readfirstlane(chunk);
     const uint32_t c = (blockIdx.y * (1u << gs) + lane) * 8u;
     const uint64_t c0 = (uint64_t)chunk * C;
-    const int32_t nrows = (int32_t)*count;
-    const uint32_t nv = (uint32_t)starts[nrows];
-    if (c0 >= nv) return;
-    const uint32_t L = kLongChunks * C;
-    uint32_t lo = (uint32_t)c0, hi = (uint32_t)(c0 + C < nv ? c0 + C : nv);
+    if (c0 >= p.n) return;
+    uint32_t lo = (uint32_t)c0, hi = (uint32_t)(c0 + C < p.n ? c0 + C : p.n);
     // the run that covers the first lookup, and the one that covers the last
-    const int32_t sf = slot[lo], sl = slot[hi - 1];
-    const uint32_t fb = (uint32_t)starts[sf], fe = (uint32_t)starts[sf + 1];
-    const uint32_t lb = (uint32_t)starts[sl], le = (uint32_t)starts[sl + 1];
-    const bool first_long = fe - fb > L, last_long = le - lb > L;
+    const int32_t sf = p.slot[lo];
+    int32_t sl = p.slot[hi - 1];
+    if (sf < 0) return;  // lookups that take no part are the last ones
+    if (sl < 0) {
+        hi = (uint32_t)p.starts[*p.count];
+        sl = p.slot[hi - 1];
+    }
+    const uint32_t fb = (uint32_t)p.starts[sf], fe = (uint32_t)p.starts[sf + 1];
+    const uint32_t lb = (uint32_t)p.starts[sl], le = (uint32_t)p.starts[sl + 1];
+    const bool first_long = fe - fb > C, last_long = le - lb > C;
     const bool from_before = fb < lo;
     if (from_before && !first_long) lo = fe;  // an earlier chunk sums it
     if (!last_long) hi = le;
@@ -450,17 +534,27 @@ __global__ __launch_bounds__(256) void grad_chunks(const int32_t *__restrict__ o
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+    // the next rows' places are read while the present rows' values arrive
+    int32_t t[U], s[U + 1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t iu = lo + u < hi ? lo + u : hi - 1;
+        t[u] = p.order[iu];
+        s[u] = p.slot[iu];
+    }
     for (uint32_t i = lo; i < hi; i += U) {
-        int32_t s[U + 1];
         typename Elem<DT>::vec8 v[U];
 #pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = load8<DT>((const typename Elem<DT>::raw *)p.dout + (uint64_t)(uint32_t)t[u] * p.stride, c, d);
+        int32_t tn[U], sn[U];
+#pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t iu = i + u < hi ? i + u : hi - 1;
-            const int32_t t = order[iu];
-            s[u] = slot[iu];
-            v[u] = load8<DT>(dout + (uint64_t)(uint32_t)t * stride, c, d);
+            const uint32_t iu = i + U + u < hi ? i + U + u : hi - 1;
+            tn[u] = p.order[iu];
+            sn[u] = p.slot[iu];
         }
-        s[U] = i + U < hi ? slot[i + U] : -1;
+        s[U] = sn[0];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (i + u < hi) {
@@ -468,68 +562,33 @@ __global__ __launch_bounds__(256) void grad_chunks(const int32_t *__restrict__ o
                 for (int e = 0; e < 8; ++e) acc[e] += Elem<DT>::get(v[u][e]);
                 if (i + u + 1 == hi || s[u + 1] != s[u]) {
                     float *row;
-                    if (s[u] == sf && first_long) row = partial + (2ull * chunk + (from_before ? 0 : 1)) * d;
-                    else if (s[u] == sl && last_long) row = partial + (2ull * chunk + 1) * d;
-                    else row = grad_row(grad, unique, rows, s[u], d);
+                    if (s[u] == sf && first_long) row = p.partial + (2ull * chunk + (from_before ? 0 : 1)) * d;
+                    else if (s[u] == sl && last_long) row = p.partial + (2ull * chunk + 1) * d;
+                    else row = grad_row(p.grad, p.unique, p.rows, s[u], d);
                     float f[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        f[e] = acc[e] * scale;
+                        f[e] = acc[e] * p.scale;
                         acc[e] = 0.0f;
                     }
                     store8<kF32>(row, c, d, f);
                 }
             }
         }
-    }
-}
-
-// The long runs: a run that begins in a chunk of this workgroup and spans more than
-// kLongChunks chunks' worth is the sum of its partial sums. 32 lanes take
-// 128 columns; the workgroup's 8 such groups every eighth partial sum.
-__global__ __launch_bounds__(256) void grad_join(const int32_t *__restrict__ slot, const int64_t *__restrict__ unique,
-                                                 const int32_t *__restrict__ starts,
-                                                 const int64_t *__restrict__ count, uint64_t rows, uint32_t d,
-                                                 const float *__restrict__ partial, float *__restrict__ grad,
-                                                 uint32_t C)
-{
-    __shared__ float sums[8][128];
-    const uint32_t nv = (uint32_t)starts[*count];
-    const uint32_t lane = threadIdx.x & 31u, g = threadIdx.x >> 5;
-    const uint32_t col = blockIdx.y * 128u + lane * 4u;
-    for (uint32_t chunk = blockIdx.x; (uint64_t)chunk * C < nv; chunk += gridDim.x) {
-        const uint64_t c0 = (uint64_t)chunk * C;
-        const uint32_t end = (uint32_t)(c0 + C < nv ? c0 + C : nv);
-        const int32_t s = slot[end - 1];
-        const uint32_t b = (uint32_t)starts[s], e = (uint32_t)starts[s + 1];
-        if (e - b <= kLongChunks * C || b < c0) continue;
-        const uint32_t parts = (e - 1) / C - chunk + 1;
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-        for (uint32_t k = g; k < parts; k += 8) {  // part 0 is this chunk's
-            const float *p = partial + (2ull * (chunk + k) + (k == 0 ? 1 : 0)) * d;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] += col + q < d ? p[col + q] : 0.0f;
+        for (int u = 0; u < U; ++u) {
+            t[u] = tn[u];
+            s[u] = sn[u];
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sums[g][lane * 4 + q] = acc[q];
-        __syncthreads();
-        if (threadIdx.x < 128) {
-            const uint32_t cc = blockIdx.y * 128u + threadIdx.x;
-            float t = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) t += sums[q][threadIdx.x];
-            if (cc < d) grad_row(grad, unique, rows, s, d)[cc] = t;
-        }
-        __syncthreads();
     }
 }
 
 // Zeros in the rows of the whole gradient that no lookup has. A workgroup
-// takes R rows, marks those that appear in unique, and fills the others.
+// takes zero_rows rows at a time, marks those that appear in unique, and
+// fills the others.
 constexpr uint32_t kZeroRowsMax = 1024;
 
-__device__ __forceinline__ uint32_t lower_bound(const int64_t *__restrict__ a, uint32_t n, int64_t v)
+__device__ __forceinline__ uint32_t lower_bound(const_i64 a, uint32_t n, int64_t v)
 {
     // the wave probes 64 places at a time: three rounds cover 2^18 entries
     uint32_t lo = 0, hi = n;  // a[lo - 1] < v <= a[hi]
@@ -548,59 +607,172 @@ __device__ __forceinline__ uint32_t lower_bound(const int64_t *__restrict__ a, u
 }
 
 template <int W>
-__global__ __launch_bounds__(256) void grad_zero(const int64_t *__restrict__ unique,
-                                                 const int64_t *__restrict__ count, uint64_t rows, uint32_t d,
-                                                 float *__restrict__ grad, uint32_t R)
+__device__ __forceinline__ void grad_zero(const GradParams &p, uint32_t first, uint32_t step)
 {
     __shared__ uint32_t seen[kZeroRowsMax / 32];
-    if (threadIdx.x < kZeroRowsMax / 32) seen[threadIdx.x] = 0;
-    const uint64_t r0 = (uint64_t)blockIdx.x * R;
-    const uint32_t nr = (uint32_t)(rows - r0 < R ? rows - r0 : R);
-    const uint32_t nu = (uint32_t)*count;
-    const uint32_t u0 = lower_bound(unique, nu, (int64_t)r0);
-    __syncthreads();
-    for (uint32_t u = u0 + threadIdx.x; u < nu; u += 256) {
-        const uint64_t r = (uint64_t)unique[u] - r0;
-        if (r >= nr) break;
-        atomicOr(&seen[r >> 5], 1u << (r & 31u));
-    }
-    __syncthreads();
-    const uint32_t per = d / W;  // W divides d
-    for (uint32_t f = threadIdx.x; f < nr * per; f += 256) {
-        const uint32_t r = f / per;
-        if (!((seen[r >> 5] >> (r & 31u)) & 1u)) {
-            float *p = grad + (r0 + r) * d + (uint64_t)(f - r * per) * W;
-            if constexpr (W == 4) {
-                typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
-                __builtin_nontemporal_store((v4)0.0f, reinterpret_cast<v4 *>(p));
-            } else {
-                __builtin_nontemporal_store(0.0f, p);
+    const uint32_t R = p.zero_rows, per = p.d / W;  // W divides d
+    const uint32_t nu = (uint32_t)*p.count;
+    const uint32_t down = 256 / per, along = 256 % per;
+    for (uint64_t r0 = (uint64_t)first * R; r0 < p.rows; r0 += (uint64_t)step * R) {
+        if (threadIdx.x < kZeroRowsMax / 32) seen[threadIdx.x] = 0;
+        const uint32_t nr = (uint32_t)(p.rows - r0 < R ? p.rows - r0 : R);
+        const uint32_t u0 = lower_bound(p.unique, nu, (int64_t)r0);
+        __syncthreads();
+        for (uint32_t u = u0 + threadIdx.x; u < nu; u += 256) {
+            const uint64_t r = (uint64_t)p.unique[u] - r0;
+            if (r >= nr) break;
+            atomicOr(&seen[r >> 5], 1u << (r & 31u));
+        }
+        __syncthreads();
+        // workgroups that run together start at different rows of their share:
+        // else their addresses, a share apart, meet in few memory channels
+        const uint32_t turn = (uint32_t)(r0 / R % nr);
+        uint32_t r = threadIdx.x / per, col = threadIdx.x % per;
+        while (r < nr) {
+            const uint32_t at = r + turn < nr ? r + turn : r + turn - nr;
+            if (!((seen[at >> 5] >> (at & 31u)) & 1u)) {
+                float *to = p.grad + (r0 + at) * p.d + (uint64_t)col * W;
+                if constexpr (W == 4) {
+                    typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
+                    *reinterpret_cast<v4 *>(to) = (v4)0.0f;
+                } else {
+                    *to = 0.0f;
+                }
+            }
+            r += down;
+            col += along;
+            if (col >= per) {
+                col -= per;
+                ++r;
             }
         }
+        __syncthreads();
     }
 }
+
+// Both in one launch, as neither waits for the other: the sums come first
+// (they take long, and few workgroups), the zeros fill what they leave idle.
+template <int DT, bool WAVE>
+__global__ __launch_bounds__(256) void grad_rows(GradParams p)
+{
+    if (blockIdx.x < p.blocks) {
+        grad_chunk_sum<DT, WAVE>(p);
+        return;
+    }
+    const uint32_t first = (blockIdx.x - p.blocks) * gridDim.y + blockIdx.y, step = (gridDim.x - p.blocks) * gridDim.y;
+    if (p.d % 4 == 0) grad_zero<4>(p, first, step);
+    else grad_zero<1>(p, first, step);
+}
+
+typedef float float4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Columns [c, c + 4) of a row of d floats, zeros past its end.
+__device__ __forceinline__ float4_any load4(const float *row, uint32_t c, uint32_t d)
+{
+    if (c + 4 <= d) return *reinterpret_cast<const float4_any *>(row + c);
+    float4_any v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = c + q < d ? row[c + q] : 0.0f;
+    return v;
+}
+
+// The long runs: each is the sum of its partial sums. A workgroup looks for
+// those that begin in its kJoinChunks chunks; 16 lanes take 64 columns, the
+// workgroup's 16 such groups every 16th partial sum.
+constexpr uint32_t kJoinChunks = 16, kJoinColumns = 64;
+
+__global__ __launch_bounds__(256) void grad_join(const int32_t *__restrict__ slot, const int64_t *__restrict__ unique,
+                                                 const int32_t *__restrict__ starts, uint64_t rows, uint32_t n,
+                                                 uint32_t d, const float *__restrict__ partial,
+                                                 float *__restrict__ grad, uint32_t C)
+{
+    __shared__ float sums[16][kJoinColumns];
+    __shared__ uint32_t found, run_chunk[kJoinChunks], run_parts[kJoinChunks];
+    __shared__ int32_t run_slot[kJoinChunks];
+    const uint32_t lane = threadIdx.x & 15u, g = threadIdx.x >> 4;
+    const uint32_t col = blockIdx.y * kJoinColumns + lane * 4u;
+    if (threadIdx.x < 64) {
+        const uint32_t chunk = blockIdx.x * kJoinChunks + (threadIdx.x & (kJoinChunks - 1u));
+        const uint64_t c0 = (uint64_t)chunk * C;
+        bool begins = false;
+        int32_t s = -1;
+        uint32_t e = 0;
+        // a long run that begins in a chunk covers its last lookup
+        if (threadIdx.x < kJoinChunks && c0 + C <= n) s = slot[c0 + C - 1];
+        if (s >= 0) {
+            const uint32_t b = (uint32_t)starts[s];
+            e = (uint32_t)starts[s + 1];
+            begins = e - b > C && b >= c0;
+        }
+        const uint64_t set = __ballot(begins);
+        if (begins) {
+            const uint32_t at = (uint32_t)__popcll(set & lanes_below());
+            run_chunk[at] = chunk;
+            run_parts[at] = (e - 1) / C - chunk + 1;
+            run_slot[at] = s;
+        }
+        if (threadIdx.x == 0) found = (uint32_t)__popcll(set);
+    }
+    __syncthreads();
+    for (uint32_t r = 0; r < found; ++r) {
+        const uint32_t chunk = run_chunk[r], parts = run_parts[r];
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (uint32_t k = g; k < parts; k += 16) {  // part 0 is this chunk's
+            const auto v = load4(partial + (2ull * (chunk + k) + (k == 0 ? 1 : 0)) * d, col, d);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] += v[q];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sums[g][lane * 4 + q] = acc[q];
+        __syncthreads();
+        const uint32_t cc = blockIdx.y * kJoinColumns + threadIdx.x;
+        if (threadIdx.x < kJoinColumns && cc < d) {
+            float t = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) t += sums[q][threadIdx.x];
+            grad_row(grad, unique, rows, run_slot[r], d)[cc] = t;
+        }
+        __syncthreads();
+    }
+}
+
+constexpr uint32_t kZeroBlocks = 1u << 20;  // workgroups that clear rows, at most
 
 template <int DT>
 hipError_t launch_grad(const EmbedGradArgs &a)
 {
-    const uint32_t C = grad_chunk(a.n), d = (uint32_t)a.d;
-    const uint32_t chunks = (uint32_t)div_up(a.n, C);
-    const int gs = row_lanes_log2(a.d);
-    float *const partial = reinterpret_cast<float *>(a.workspace);
+    GradParams p{};
+    p.order = (const_i32)a.order;
+    p.slot = (const_i32)a.slot;
+    p.unique = (const_i64)a.unique;
+    p.starts = (const_i32)a.starts;
+    p.count = (const_i64)a.count;
+    p.rows = a.rows;
+    p.dout = a.dout;
+    p.n = (uint32_t)a.n;
+    p.d = (uint32_t)a.d;
+    p.stride = a.stride;
+    p.scale = a.scale;
+    p.grad = a.grad;
+    p.partial = reinterpret_cast<float *>(a.workspace);
+    p.C = grad_chunk(a.n);
+    p.gs = row_lanes_log2(a.d);
+    const uint64_t chunks = div_up(a.n, p.C);
+    const uint32_t slices = (uint32_t)div_up(a.d, 8ull << p.gs);
+    p.blocks = (uint32_t)div_up(chunks, 256u >> p.gs);
+    uint32_t blocks = p.blocks;
     if (a.rows) {
-        uint32_t R = 65536u / d;  // about 256 KiB of gradient per workgroup
-        R = R < 1 ? 1 : R > kZeroRowsMax ? kZeroRowsMax : R;
-        const uint32_t blocks = (uint32_t)div_up(a.rows, R);
-        if (d % 4 == 0) grad_zero<4><<<blocks, 256, 0, a.stream>>>(a.unique, a.count, a.rows, d, a.grad, R);
-        else grad_zero<1><<<blocks, 256, 0, a.stream>>>(a.unique, a.count, a.rows, d, a.grad, R);
+        const uint64_t R = 16384u / a.d;  // 64 KiB of gradient per workgroup: several rounds of them hide the search
+        p.zero_rows = (uint32_t)(R < 1 ? 1 : R > kZeroRowsMax ? kZeroRowsMax : R);
+        const uint64_t zero = div_up(div_up(a.rows, p.zero_rows), slices), most = div_up(kZeroBlocks, slices);
+        blocks += (uint32_t)(zero < most ? zero : most);
     }
-    if (a.n == 0) return hipGetLastError();
-    grad_chunks<DT><<<dim3((uint32_t)div_up(chunks, 256u >> gs), (uint32_t)div_up(a.d, 8ull << gs)), 256, 0,
-                      a.stream>>>(a.order, a.slot, a.unique, a.starts, a.count, a.rows,
-                                  (const typename Elem<DT>::raw *)a.dout, d, a.stride, a.scale, a.grad, partial, C, gs);
-    if (a.n > (uint64_t)kLongChunks * C)
-        grad_join<<<dim3(chunks < 65536u ? chunks : 65536u, (uint32_t)div_up(a.d, 128)), 256, 0, a.stream>>>(
-            a.slot, a.unique, a.starts, a.count, a.rows, d, partial, a.grad, C);
+    if (p.gs == 6) grad_rows<DT, true><<<dim3(blocks, slices), 256, 0, a.stream>>>(p);
+    else grad_rows<DT, false><<<dim3(blocks, slices), 256, 0, a.stream>>>(p);
+    if (a.n > p.C)
+        grad_join<<<dim3((uint32_t)div_up(chunks, kJoinChunks), (uint32_t)div_up(a.d, kJoinColumns)), 256, 0,
+                    a.stream>>>(a.slot, a.unique, a.starts, a.rows, p.n, p.d, p.partial, a.grad, p.C);
     return hipGetLastError();
 }
 

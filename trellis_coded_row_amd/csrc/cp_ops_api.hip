@@ -6,6 +6,7 @@
 
 static constexpr uint64_t kMaxCount = 0x7FFFFFFFull;           // lengths that kernels hold in 32 bits
 static constexpr uint64_t kMaxSorted = 0x7FFFFFFFull - 4095;   // ids of one plan
+static constexpr uint64_t kMaxGradColumns = 1ull << 21;        // a launch has fewer than 2^16 workgroups along y
 static constexpr uint64_t kMaxGemmStride = 1ull << 22;         // a tile's rows then lie within 2^31 bytes
 static constexpr uint64_t kMaxGemmRows = 1ull << 25;         // launches then have fewer than 2^32 threads
 
@@ -94,7 +95,7 @@ cp_status cp_embed_plan(const int64_t *ids, uint64_t n, uint64_t rows, int32_t *
 
 uint64_t cp_embed_grad_workspace_bytes(uint64_t n, uint64_t d)
 {
-    if (n > kMaxSorted || d > kMaxSorted) return 0;
+    if (n > kMaxSorted || d > kMaxGradColumns) return 0;
     return cpk::embed_grad_workspace_bytes(n, d);
 }
 
@@ -104,6 +105,7 @@ cp_status cp_embed_grad(const int32_t *order, const int32_t *slot, const int64_t
                         void *stream)
 {
     if (!dtype_ok(dtype) || n > kMaxSorted || d > kMaxSorted) return CP_ERR_INVALID_ARGUMENT;
+    if (d > kMaxGradColumns) return CP_ERR_UNSUPPORTED;
     if (rows > (1ull << 62) || !spans(rows, d, 4) || !spans(n, dout_stride, 4)) return CP_ERR_INVALID_ARGUMENT;
     if (d == 0 || (n == 0 && rows == 0)) return CP_OK;
     if (!good(starts, 4) || !good(count, 8) || !good(grad, 4)) return CP_ERR_INVALID_ARGUMENT;
