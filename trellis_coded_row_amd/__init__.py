@@ -592,7 +592,9 @@ class MixedTable(Table):
         return out
 
 
-# the dense operators: ops.py builds on the names above
+# the dense operators: ops.py builds on the names above, and on a library of its own
+if not os.path.exists(_build.TORCH_LIB):
+    _build.build_torch()
 from . import ops as _ops  # noqa: E402
 from .ops import *  # noqa: E402,F401,F403
 

@@ -1,11 +1,14 @@
 """Builds the HIP libraries for gfx950 with hipcc, in-tree: libcp.so (the
-lookup library, include/cp.h and include/cp_ops.h) and libcp_probe.so (measurement probes,
-include/cp_probe.h)."""
+lookup library, include/cp.h and include/cp_ops.h), libcp_probe.so (measurement
+probes, include/cp_probe.h) and _cp_torch.so (the dense operators' functions on
+torch tensors, host code on top of libcp.so)."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +26,8 @@ DEPS = SOURCES + [os.path.join(CSRC, "cp_internal.h"), os.path.join(CSRC, "cp_la
 LIB = os.path.join(PKG, "libcp.so")
 PROBE_SOURCES = [os.path.join(CSRC, "cp_probe.hip")]
 PROBE_LIB = os.path.join(PKG, "libcp_probe.so")
+TORCH_SOURCE = os.path.join(CSRC, "cp_torch.cpp")
+TORCH_LIB = os.path.join(PKG, "_cp_torch.so")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -50,20 +55,42 @@ def is_stale() -> bool:
 def _hipcc(sources: list[str], lib: str, verbose: bool, extra_flags: list[str] | None) -> str:
     tmp = lib + ".tmp%d" % os.getpid()
     cmd = [hipcc(), *HIPCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), *sources, "-o", tmp]
+    return _run(cmd, tmp, lib, verbose)
+
+
+def _run(cmd: list[str], tmp: str, lib: str, verbose: bool) -> str:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed building {os.path.basename(lib)}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed building {os.path.basename(lib)}")
     os.replace(tmp, lib)
     return lib
 
 
 def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Builds both libraries; returns the path of libcp.so."""
+    """Builds the libraries; returns the path of libcp.so."""
     _hipcc(PROBE_SOURCES, PROBE_LIB, verbose, extra_flags)
-    return _hipcc(SOURCES, LIB, verbose, extra_flags)
+    lib = _hipcc(SOURCES, LIB, verbose, extra_flags)
+    build_torch(verbose)
+    return lib
+
+
+def build_torch(verbose: bool = False) -> str:
+    """Builds _cp_torch.so, a CPython module, against the torch that is
+    installed and libcp.so beside it."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]  # its folder, without importing it
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc()))) if os.path.isabs(hipcc()) else "/opt/rocm"
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
+    tmp = TORCH_LIB + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D__HIP_PLATFORM_AMD__=1",  # what hipcc itself defines; the HIP headers ask for it
+           *(x for d in include for x in ("-isystem", d)), TORCH_SOURCE, "-o", tmp,
+           "-L", PKG, "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"),
+           "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    return _run(cmd, tmp, TORCH_LIB, verbose)
 
 
 if __name__ == "__main__":
