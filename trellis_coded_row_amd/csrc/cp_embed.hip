@@ -28,73 +28,46 @@ int row_lanes_log2(uint64_t d)
 // ---------------------------------------------------------------- lookup
 
 // 2^gs lanes take a row, 8 elements each; blockIdx.y + slice0: a slice of
-// 8 << gs columns. Workgroup b takes groups of U (256 >> gs) rows: the b-th, the one
-// gridDim.x further, and so on. Where a batch has more groups than the chip
-// holds workgroups, a group's rows are read while the one before is written,
-// and its ids before that. WAVE: gs is 6, so that the ids are the same in
-// all of a wave's lanes and go through scalar registers and loads.
+// 8 << gs columns. A thread has U rows' loads in flight. WAVE: gs is 6, so
+// that the ids are the same in all of a wave's lanes and go through scalar
+// registers and loads.
 template <int TI, int TO, int U, bool WAVE>
 __global__ __launch_bounds__(256) void lookup_rows(const typename Elem<TI>::raw *__restrict__ table, uint64_t rows,
-                                                   uint32_t d, uint64_t stride, const_i64 ids,
-                                                   uint32_t n, float scale, typename Elem<TO>::raw *__restrict__ out,
+                                                   uint32_t d, uint64_t stride, const_i64 ids, uint32_t n, float scale,
+                                                   typename Elem<TO>::raw *__restrict__ out,
                                                    int32_t *__restrict__ bad_id, int gs, uint32_t slice0)
 {
-    typedef typename Elem<TI>::vec8 V;
     if constexpr (WAVE) gs = 6;
     const uint32_t per = 256u >> gs;
     const uint32_t c = (((slice0 + blockIdx.y) << gs) + (threadIdx.x & ((1u << gs) - 1u))) * 8u;
-    const uint32_t step = gridDim.x * U * per;  // below 2^22, and n below 2^31
     uint32_t j = blockIdx.x * (U * per) + (threadIdx.x >> gs);
     if constexpr (WAVE) j = __builtin_amdgcn_readfirstlane(j);
     if (c >= d) return;
-    int64_t id[U], after[U];
-    V v[U];
-    const auto read_ids = [&](uint32_t at, int64_t *to) {
+    int64_t id[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) to[u] = at + u * per < n ? ids[at + u * per] : -1;
-    };
-    const auto read_rows = [&](int64_t *of, V *to) {
+    for (int u = 0; u < U; ++u) id[u] = j + u * per < n ? ids[j + u * per] : -1;
+    typename Elem<TI>::vec8 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (of[u] >= 0 && (uint64_t)of[u] >= rows) {
-                of[u] = -1;
-                if (bad_id) *bad_id = 1;
-            }
-            if (of[u] >= 0) to[u] = load8<TI>(table + (uint64_t)of[u] * stride, c, d);
-            else to[u] = (typename Elem<TI>::raw)0;
+    for (int u = 0; u < U; ++u) {
+        if (id[u] >= 0 && (uint64_t)id[u] >= rows) {
+            id[u] = -1;
+            if (bad_id) *bad_id = 1;
         }
-    };
-    read_ids(j, id);
-    read_rows(id, v);
-    read_ids(j + step, after);
-    while (j < n) {
-        V next[U];
-        bool none[U];
+        if (id[u] >= 0) v[u] = load8<TI>(table + (uint64_t)id[u] * stride, c, d);
+        else v[u] = (typename Elem<TI>::raw)0;
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) none[u] = id[u] < 0;
-        if (j + step < n) {
+    for (int u = 0; u < U; ++u) {
+        if (j + u * per >= n) continue;
+        float f[8];
 #pragma unroll
-            for (int u = 0; u < U; ++u) id[u] = after[u];
-            read_rows(id, next);
-            read_ids(j + 2 * step, after);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (j + u * per >= n) continue;
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = none[u] ? 0.0f : Elem<TI>::get(v[u][e]) * scale;  // padding: +0 for any scale
-            store8<TO, true>(out + (uint64_t)(j + u * per) * d, c, d, f);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = next[u];
-        j += step;
+        for (int e = 0; e < 8; ++e) f[e] = id[u] < 0 ? 0.0f : Elem<TI>::get(v[u][e]) * scale;  // padding: +0 for any scale
+        store8<TO, true>(out + (uint64_t)(j + u * per) * d, c, d, f);
     }
 }
 
-// Workgroups that stay: as many as the registers let each compute unit hold.
-constexpr uint32_t kLookupBlocksWave = 256 * 8, kLookupBlocks = 256 * 4;
-constexpr uint32_t kLookupSlices = 4096;  // slices of one launch, at most (it has fewer than 2^32 threads)
+constexpr uint32_t kLookupBlocks = 1u << 22;  // workgroups of one launch, at most
+constexpr uint32_t kManyRows = 8;             // rows of a thread where there are many
 
 template <int TI, int TO>
 hipError_t launch_lookup(const EmbedLookupArgs &a)
@@ -102,20 +75,26 @@ hipError_t launch_lookup(const EmbedLookupArgs &a)
     typedef typename Elem<TI>::raw RI;
     typedef typename Elem<TO>::raw RO;
     const int gs = row_lanes_log2(a.d);
-    const uint32_t per = 256u >> gs, slices = (uint32_t)div_up(a.d, 8ull << gs);
-    // four rows in flight per thread once that still fills the chip
-    const uint32_t most = gs == 6 ? kLookupBlocksWave : kLookupBlocks;
-    const bool four = a.n >= 4ull * per * most;
-    const uint64_t groups = div_up(a.n, (four ? 4ull : 1ull) * per);
-    const uint32_t blocks = (uint32_t)(groups < most ? groups : most);
-    for (uint32_t y = 0; y < slices; y += kLookupSlices) {
-        const dim3 grid(blocks, slices - y < kLookupSlices ? slices - y : kLookupSlices);
-        const auto launch = [&](auto kernel) {
-            kernel<<<grid, 256, 0, a.stream>>>((const RI *)a.table, a.rows, (uint32_t)a.d, a.row_stride,
-                                               (const_i64)a.ids, (uint32_t)a.n, a.scale, (RO *)a.out, a.bad_id, gs, y);
-        };
-        if (gs == 6) four ? launch(lookup_rows<TI, TO, 4, true>) : launch(lookup_rows<TI, TO, 1, true>);
-        else four ? launch(lookup_rows<TI, TO, 4, false>) : launch(lookup_rows<TI, TO, 1, false>);
+    const uint32_t per = 256u >> gs;
+    const uint64_t slices = div_up(a.d, 8ull << gs);
+    // many rows per thread once that still leaves the chip several
+    // workgroups per compute unit
+    const bool many = a.n >= (uint64_t)kManyRows * per * 2048;
+    const uint32_t each = (many ? kManyRows : 1) * per;
+    // a launch has fewer than 2^32 threads, and fewer than 2^16 workgroups along y
+    const uint64_t step_y = slices < 16384 ? slices : 16384, step = kLookupBlocks / step_y * each;
+    for (uint64_t y = 0; y < slices; y += step_y) {
+        for (uint64_t j = 0; j < a.n; j += step) {
+            const uint32_t n = (uint32_t)(a.n - j < step ? a.n - j : step);
+            const dim3 grid((uint32_t)div_up(n, each), (uint32_t)(slices - y < step_y ? slices - y : step_y));
+            const auto launch = [&](auto kernel) {
+                kernel<<<grid, 256, 0, a.stream>>>((const RI *)a.table, a.rows, (uint32_t)a.d, a.row_stride,
+                                                   (const_i64)(a.ids + j), n, a.scale, (RO *)a.out + j * a.d, a.bad_id, gs,
+                                                   (uint32_t)y);
+            };
+            if (gs == 6) many ? launch(lookup_rows<TI, TO, kManyRows, true>) : launch(lookup_rows<TI, TO, 1, true>);
+            else many ? launch(lookup_rows<TI, TO, kManyRows, false>) : launch(lookup_rows<TI, TO, 1, false>);
+        }
     }
     return hipGetLastError();
 }
@@ -491,10 +470,8 @@ struct GradParams {
     uint64_t stride;
     float scale;
     float *grad, *partial;
-    uint32_t C;       // lookups per chunk
-    int gs;           // 2^gs lanes per chunk
-    uint32_t blocks;  // workgroups along x that sum chunks; those after it clear rows
-    uint32_t zero_rows;
+    uint32_t C;  // lookups per chunk
+    int gs;      // 2^gs lanes per chunk
 };
 
 // Chunk c: sorted lookups [c C, c C + C). Its group of 2^gs lanes sums the
@@ -504,7 +481,7 @@ struct GradParams {
 // columns. WAVE: gs is 6, so that everything but the row's values is the same
 // in all of a wave's lanes and goes through scalar registers and loads.
 template <int DT, bool WAVE>
-__device__ __forceinline__ void grad_chunk_sum(const GradParams &p)
+__global__ __launch_bounds__(256) void grad_rows(GradParams p)
 {
     constexpr int U = 8;  // rows' loads in flight
     const int gs = WAVE ? 6 : p.gs;
@@ -583,85 +560,24 @@ __device__ __forceinline__ void grad_chunk_sum(const GradParams &p)
     }
 }
 
-// Zeros in the rows of the whole gradient that no lookup has. A workgroup
-// takes zero_rows rows at a time, marks those that appear in unique, and
-// fills the others.
-constexpr uint32_t kZeroRowsMax = 1024;
+// Zeros in the whole gradient, before the sums are written: bound by the
+// stores. One of 16 bytes for each thread of a workgroup that ends then is
+// the fastest (131,072 x 1,024: 79 us, 6.8 TB/s; workgroups that clear 64 KiB
+// each 99 us), faster than leaving out the rows that sums go to, which has to
+// look each up (107 us).
+constexpr uint32_t kZeroFloats = 1024;  // of a workgroup
 
-__device__ __forceinline__ uint32_t lower_bound(const_i64 a, uint32_t n, int64_t v)
+__global__ __launch_bounds__(256) void grad_zero(float *__restrict__ grad, uint64_t count)
 {
-    // the wave probes 64 places at a time: three rounds cover 2^18 entries
-    uint32_t lo = 0, hi = n;  // a[lo - 1] < v <= a[hi]
-    while (lo < hi) {
-        const uint32_t step = (hi - lo + 63) / 64;
-        const uint64_t at = (uint64_t)lo + (uint64_t)(threadIdx.x & 63u) * step;
-        const bool less = at < hi && a[at] < v;
-        const uint32_t k = (uint32_t)__popcll(__ballot(less));  // a prefix of the lanes
-        if (k == 0) return lo;
-        const uint64_t nlo = (uint64_t)lo + (uint64_t)(k - 1) * step + 1;
-        const uint64_t nhi = (uint64_t)lo + (uint64_t)k * step;
-        lo = (uint32_t)nlo;
-        hi = (uint32_t)(nhi < hi ? nhi : hi);
-    }
-    return lo;
-}
-
-template <int W>
-__device__ __forceinline__ void grad_zero(const GradParams &p, uint32_t first, uint32_t step)
-{
-    __shared__ uint32_t seen[kZeroRowsMax / 32];
-    const uint32_t R = p.zero_rows, per = p.d / W;  // W divides d
-    const uint32_t nu = (uint32_t)*p.count;
-    const uint32_t down = 256 / per, along = 256 % per;
-    for (uint64_t r0 = (uint64_t)first * R; r0 < p.rows; r0 += (uint64_t)step * R) {
-        if (threadIdx.x < kZeroRowsMax / 32) seen[threadIdx.x] = 0;
-        const uint32_t nr = (uint32_t)(p.rows - r0 < R ? p.rows - r0 : R);
-        const uint32_t u0 = lower_bound(p.unique, nu, (int64_t)r0);
-        __syncthreads();
-        for (uint32_t u = u0 + threadIdx.x; u < nu; u += 256) {
-            const uint64_t r = (uint64_t)p.unique[u] - r0;
-            if (r >= nr) break;
-            atomicOr(&seen[r >> 5], 1u << (r & 31u));
+    typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
+    for (uint64_t at = (uint64_t)blockIdx.x * kZeroFloats + threadIdx.x * 4u; at < count;
+         at += (uint64_t)gridDim.x * kZeroFloats) {
+        if (at + 4 <= count) {
+            *reinterpret_cast<v4 *>(grad + at) = (v4)0.0f;
+        } else {
+            for (uint64_t q = at; q < count; ++q) grad[q] = 0.0f;
         }
-        __syncthreads();
-        // workgroups that run together start at different rows of their share:
-        // else their addresses, a share apart, meet in few memory channels
-        const uint32_t turn = (uint32_t)(r0 / R % nr);
-        uint32_t r = threadIdx.x / per, col = threadIdx.x % per;
-        while (r < nr) {
-            const uint32_t at = r + turn < nr ? r + turn : r + turn - nr;
-            if (!((seen[at >> 5] >> (at & 31u)) & 1u)) {
-                float *to = p.grad + (r0 + at) * p.d + (uint64_t)col * W;
-                if constexpr (W == 4) {
-                    typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
-                    *reinterpret_cast<v4 *>(to) = (v4)0.0f;
-                } else {
-                    *to = 0.0f;
-                }
-            }
-            r += down;
-            col += along;
-            if (col >= per) {
-                col -= per;
-                ++r;
-            }
-        }
-        __syncthreads();
     }
-}
-
-// Both in one launch, as neither waits for the other: the sums come first
-// (they take long, and few workgroups), the zeros fill what they leave idle.
-template <int DT, bool WAVE>
-__global__ __launch_bounds__(256) void grad_rows(GradParams p)
-{
-    if (blockIdx.x < p.blocks) {
-        grad_chunk_sum<DT, WAVE>(p);
-        return;
-    }
-    const uint32_t first = (blockIdx.x - p.blocks) * gridDim.y + blockIdx.y, step = (gridDim.x - p.blocks) * gridDim.y;
-    if (p.d % 4 == 0) grad_zero<4>(p, first, step);
-    else grad_zero<1>(p, first, step);
 }
 
 typedef float float4_any __attribute__((ext_vector_type(4), aligned(4)));
@@ -737,8 +653,6 @@ __global__ __launch_bounds__(256) void grad_join(const int32_t *__restrict__ slo
     }
 }
 
-constexpr uint32_t kZeroBlocks = 1u << 20;  // workgroups that clear rows, at most
-
 template <int DT>
 hipError_t launch_grad(const EmbedGradArgs &a)
 {
@@ -760,16 +674,15 @@ hipError_t launch_grad(const EmbedGradArgs &a)
     p.gs = row_lanes_log2(a.d);
     const uint64_t chunks = div_up(a.n, p.C);
     const uint32_t slices = (uint32_t)div_up(a.d, 8ull << p.gs);
-    p.blocks = (uint32_t)div_up(chunks, 256u >> p.gs);
-    uint32_t blocks = p.blocks;
     if (a.rows) {
-        const uint64_t R = 16384u / a.d;  // 64 KiB of gradient per workgroup: several rounds of them hide the search
-        p.zero_rows = (uint32_t)(R < 1 ? 1 : R > kZeroRowsMax ? kZeroRowsMax : R);
-        const uint64_t zero = div_up(div_up(a.rows, p.zero_rows), slices), most = div_up(kZeroBlocks, slices);
-        blocks += (uint32_t)(zero < most ? zero : most);
+        const uint64_t count = a.rows * a.d, blocks = div_up(count, kZeroFloats);
+        // (a launch has fewer than 2^32 threads)
+        grad_zero<<<(uint32_t)(blocks < (1u << 23) ? blocks : 1u << 23), 256, 0, a.stream>>>(a.grad, count);
     }
-    if (p.gs == 6) grad_rows<DT, true><<<dim3(blocks, slices), 256, 0, a.stream>>>(p);
-    else grad_rows<DT, false><<<dim3(blocks, slices), 256, 0, a.stream>>>(p);
+    if (a.n == 0) return hipGetLastError();
+    const dim3 grid((uint32_t)div_up(chunks, 256u >> p.gs), slices);
+    if (p.gs == 6) grad_rows<DT, true><<<grid, 256, 0, a.stream>>>(p);
+    else grad_rows<DT, false><<<grid, 256, 0, a.stream>>>(p);
     if (a.n > p.C)
         grad_join<<<dim3((uint32_t)div_up(chunks, kJoinChunks), (uint32_t)div_up(a.d, kJoinColumns)), 256, 0,
                     a.stream>>>(a.slot, a.unique, a.starts, a.rows, p.n, p.d, p.partial, a.grad, p.C);
