@@ -103,7 +103,7 @@ hipError_t launch_lookup(const EmbedLookupArgs &a)
 
 constexpr uint32_t kSortThreads = 512;
 constexpr uint32_t kSortWaves = kSortThreads / 64;
-constexpr uint32_t kSortRounds = 4;                            // keys per thread
+constexpr uint32_t kSortRounds = 2;                            // keys per thread
 constexpr uint32_t kSortTile = kSortThreads * kSortRounds;     // keys per workgroup
 constexpr int kDigitBits = 9;                                  // bits sorted by one pass, at most
 constexpr uint32_t kDigits = 1u << kDigitBits;
@@ -633,7 +633,7 @@ __global__ __launch_bounds__(256) void grad_join(const int32_t *__restrict__ slo
     for (uint32_t r = 0; r < found; ++r) {
         const uint32_t chunk = run_chunk[r], parts = run_parts[r];
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
+#pragma unroll 16
         for (uint32_t k = g; k < parts; k += 16) {  // part 0 is this chunk's
             const auto v = load4(partial + (2ull * (chunk + k) + (k == 0 ? 1 : 0)) * d, col, d);
 #pragma unroll
