@@ -158,6 +158,7 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
     constexpr int FB = FN < 4 ? FN : 4, NG = FM / 2;
     constexpr bool IN_PLACE = !EXACT && FM * FN == 64;
     constexpr int LA = BM / 32, LB = BN / 32;  // copies of 8 rows per wave
+    constexpr bool SPREAD = !EXACT && FM == 8 && FN == 8;
     __shared__ __attribute__((aligned(16))) uint8_t as0[BM * kStep], as1[BM * kStep], bs0[BN * kStep],
         bs1[BN * kStep];
     const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -212,6 +213,17 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
             const uint32_t v = KTAIL && k0 + cb[i] >= p.k ? kOutside : vb[i];
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(bs + (w * LB + i) * 1024), 16, v, k0, 0, 0);
         }
+    };
+    // one of this wave's copies of 8 rows
+    [[maybe_unused]] const auto copy_a = [&](uint32_t s, uint8_t *as, int i) {
+        const uint32_t k0 = s * kStep, v = KTAIL && k0 + ca[i] >= p.k ? kOutside : va[i];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(pa, s < s1 ? kInside : 0),
+                                                 (lds_void *)(as + (w * LA + i) * 1024), 16, v, k0, 0, 0);
+    };
+    [[maybe_unused]] const auto copy_b = [&](uint32_t s, uint8_t *bs, int i) {
+        const uint32_t k0 = s * kStep, v = KTAIL && k0 + cb[i] >= p.k ? kOutside : vb[i];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(pb, s < s1 ? kInside : 0),
+                                                 (lds_void *)(bs + (w * LB + i) * 1024), 16, v, k0, 0, 0);
     };
     const auto copy = [&](uint32_t s, uint8_t *as, uint8_t *bs) {
 #pragma unroll
@@ -290,15 +302,32 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
                 af[cur ^ 1][0] = read_a(as, 2 * ag + 2);
                 af[cur ^ 1][1] = read_a(as, 2 * ag + 3);
             } else {
-                __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's LDS reads and copies are done
-                __syncthreads();
+                // this wave's LDS reads and copies are done (where they are
+                // spread: but for the last LB, of B's step after the next)
+                if constexpr (SPREAD) {
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LB) : "memory");
+                } else {
+                    __builtin_amdgcn_s_waitcnt(0x0070);
+                    __syncthreads();
+                }
                 if (partial_chunk && s + 2 == s1) clear_tail(an, bn);
                 af[cur ^ 1][0] = read_a(an, 0);
                 af[cur ^ 1][1] = read_a(an, 1);
             }
+            // every wave holds its part of B: its place is free
+            if (SPREAD && ag == 1) asm volatile("s_barrier" ::: "memory");
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
-                if (ag + 1 == NG) copy_share(s + 2, as, bs, f);  // one share before each pair of products
+                if constexpr (SPREAD) {  // a copy before every other pair of products
+                    if (f % 2 == 0) {
+                        const int i = f / 2;
+                        if (ag + 1 == NG) copy_a(s + 2, as, i);
+                        else if (ag == 0) copy_a(s + 1, an, LA / 2 + i);
+                        else copy_b(s + 2, bs, (ag - 1) * (LB / 2) + i);
+                    }
+                } else if (ag + 1 == NG) {
+                    copy_share(s + 2, as, bs, f);  // one share before each pair of products
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int i = 2 * ag + h;
@@ -383,7 +412,14 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
     __builtin_amdgcn_s_waitcnt(0x0070);
     __syncthreads();
     if (partial_chunk && steps == 1) clear_tail(as0, bs0);
-    copy(s0 + 1, as1, bs1);
+    if constexpr (SPREAD) {
+#pragma unroll
+        for (int i = 0; i < LB; ++i) copy_b(s0 + 1, bs1, i);
+#pragma unroll
+        for (int i = 0; i < LA / 2; ++i) copy_a(s0 + 1, as1, i);
+    } else {
+        copy(s0 + 1, as1, bs1);
+    }
     if constexpr (EXACT) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -428,6 +464,7 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
         }
         s += 2;
     } while (s < s1);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // the copies past the end (zeros) are in LDS while it is this workgroup's
 
     if constexpr (IN_PLACE) {
         settle();
