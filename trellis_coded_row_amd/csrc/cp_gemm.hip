@@ -132,6 +132,35 @@ struct TileParams {
     int out_dtype;
 };
 
+// A workgroup's tile and its steps of k.
+struct TilePlace {
+    uint32_t m0, n0, split, s0, s1;
+};
+
+__device__ __forceinline__ TilePlace place_of(const TileParams &p, uint32_t BM, uint32_t BN)
+{
+    // workgroup id -> tile: each of the 8 XCDs (ids taken in turn) gets a
+    // contiguous run of tiles, which go down 8 tile rows at a time, so that
+    // the operands an XCD reads at one time are few enough for its own L2
+    const uint32_t ntiles = p.tiles_m * p.tiles_n, total = gridDim.x;
+    const uint32_t xcd = blockIdx.x & 7u, per = total >> 3, extra = total & 7u;
+    const uint32_t id = xcd * per + (xcd < extra ? xcd : extra) + (blockIdx.x >> 3);
+    // (the quotients come out of vector registers: back to scalar ones)
+    const uint32_t split = __builtin_amdgcn_readfirstlane(id / ntiles), tile = id - split * ntiles;
+    const uint32_t band = __builtin_amdgcn_readfirstlane(tile / (8 * p.tiles_n)), band_m = band * 8;
+    const uint32_t band_rows = p.tiles_m - band_m < 8 ? p.tiles_m - band_m : 8;
+    const uint32_t in_band = tile - band * 8 * p.tiles_n;
+    const uint32_t column = __builtin_amdgcn_readfirstlane(in_band / band_rows);
+    TilePlace t;
+    t.m0 = (band_m + in_band - column * band_rows) * BM;
+    t.n0 = column * BN;
+    const uint32_t all_steps = (p.k + kStep - 1) / kStep;
+    t.split = split;
+    t.s0 = split * p.steps_per_split;
+    t.s1 = t.s0 + p.steps_per_split < all_steps ? t.s0 + p.steps_per_split : all_steps;
+    return t;
+}
+
 // Tiles of 32 FM x 32 FN outputs; four waves, 2 x 2, each with FM x FN
 // fragments of 16 x 16. A step's operands (128 values of k) are copied to
 // LDS by loads that bypass the registers, one step ahead, into the other of
@@ -163,22 +192,9 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
         bs1[BN * kStep];
     const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t wm = w >> 1, wn = w & 1u, r = lane & 15u, g = lane >> 4;
-    // workgroup id -> tile: each of the 8 XCDs (ids taken in turn) gets a
-    // contiguous run of tiles, which go down 8 tile rows at a time, so that
-    // the operands an XCD reads at one time are few enough for its own L2
-    const uint32_t ntiles = p.tiles_m * p.tiles_n, total = gridDim.x;
-    const uint32_t xcd = blockIdx.x & 7u, per = total >> 3, extra = total & 7u;
-    const uint32_t id = xcd * per + (xcd < extra ? xcd : extra) + (blockIdx.x >> 3);
-    // (the quotients come out of vector registers: back to scalar ones)
-    const uint32_t split = __builtin_amdgcn_readfirstlane(id / ntiles), tile = id - split * ntiles;
-    const uint32_t band = __builtin_amdgcn_readfirstlane(tile / (8 * p.tiles_n)), band_m = band * 8;
-    const uint32_t band_rows = p.tiles_m - band_m < 8 ? p.tiles_m - band_m : 8;
-    const uint32_t in_band = tile - band * 8 * p.tiles_n;
-    const uint32_t column = __builtin_amdgcn_readfirstlane(in_band / band_rows);
-    const uint32_t m0 = (band_m + in_band - column * band_rows) * BM, n0 = column * BN;
+    const TilePlace place = place_of(p, BM, BN);
+    const uint32_t m0 = place.m0, n0 = place.n0, s0 = place.s0, s1 = place.s1;
     const uint32_t all_steps = (p.k + kStep - 1) / kStep;
-    const uint32_t s0 = split * p.steps_per_split;
-    const uint32_t s1 = s0 + p.steps_per_split < all_steps ? s0 + p.steps_per_split : all_steps;
     const uint32_t steps = s1 - s0;
 
     const uint8_t *const pa = p.a + (uint64_t)m0 * p.a_stride, *const pb = p.b + (uint64_t)n0 * p.b_stride;
@@ -473,7 +489,7 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
 #pragma unroll
             for (int f = 0; f < FN; ++f) asm volatile("" : "+a"(acc[i][f]));
     }
-    void *const out = p.out_dtype == kF32 ? (void *)((float *)p.out + split * p.split_stride) : p.out;
+    void *const out = p.out_dtype == kF32 ? (void *)((float *)p.out + place.split * p.split_stride) : p.out;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const uint32_t row = m0 + wm * FM * 16 + i * 16 + r;
@@ -488,6 +504,271 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
                 for (int e = 0; e < 8; ++e) o[e] = acc[i][q * FB + 2 * h + (e >> 2)][e & 3];
                 put_out(out, p.out_dtype, row, p.out_stride, c + 8 * h, p.n, o);
             }
+        }
+    }
+}
+
+// 32-bit outputs of large matrices: tiles of 256 x 128 as above, with the
+// 32 x 32 bf16 instruction (measured on one unit: 1,011 operations per cycle,
+// the 16 x 16 one 600). Four waves, 2 x 2, each with 4 x 2 fragments of
+// 32 x 32: lane l carries row l % 32 and the 16-byte chunks l / 32 + 2 j
+// (j < 4) of its 128 values. A step goes by A's fragments, 16 products each;
+// the next fragment is widened, and the one after it read, under them.
+//
+// LDS: chunk c of A's row r stands at c ^ (r / 2 % 8). B's fragment f has the
+// rows n = 32 (r / 4 % 2) + 8 (r / 8) + 4 f + r % 4 of its wave's 64, so that a
+// lane's results are 32 neighbours in its output row; chunk c of row n stands
+// at c ^ (bits 1, 5 and 3 of n): the 16 lanes that a read serves together have
+// each of the 8 values twice, with an even row and with an odd one.
+struct Raw {
+    i32x4 c[4];
+};
+
+// 64 scaled e4m3 values in bf16: piece k is half k % 2 of chunk k / 2.
+struct Wide64 {
+    bf16x8 v[8];
+};
+
+__device__ __forceinline__ bf16x8 widen_piece(const Raw &x, int k, float scale)
+{
+    const int lo = x.c[k >> 1][2 * (k & 1)], hi = x.c[k >> 1][2 * (k & 1) + 1];
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <bool BLOCKS, bool KTAIL>
+__global__ __launch_bounds__(256) void gemm_wide(TileParams p)
+{
+    constexpr uint32_t BM = 256, BN = 128;
+    constexpr int LA = BM / 32, LB = BN / 32;  // copies of 8 rows per wave
+    __shared__ __attribute__((aligned(16))) uint8_t as0[BM * kStep], as1[BM * kStep], bs0[BN * kStep],
+        bs1[BN * kStep];
+    const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t wm = w >> 1, wn = w & 1u, r = lane & 31u, g = lane >> 5;
+    const TilePlace at = place_of(p, BM, BN);
+    const uint32_t m0 = at.m0, n0 = at.n0, s0 = at.s0, s1 = at.s1;
+    const uint32_t all_steps = (p.k + kStep - 1) / kStep;
+
+    const uint8_t *const pa = p.a + (uint64_t)m0 * p.a_stride, *const pb = p.b + (uint64_t)n0 * p.b_stride;
+    const auto key_a = [](uint32_t row) { return (row >> 1) & 7u; };
+    const auto key_b = [](uint32_t row) { return ((row >> 1) & 1u) | ((row >> 4) & 2u) | ((row >> 1) & 4u); };
+    // where this lane's part of each copy comes from (rows past the end: the last one)
+    uint32_t va[LA], vb[LB], ca[LA], cb[LB];
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const uint32_t row = (w * LA + i) * 8 + (lane >> 3), in = m0 + row < p.m ? row : p.m - 1 - m0;
+        ca[i] = ((lane & 7u) ^ key_a(row)) * 16;
+        va[i] = in * p.a_stride + ca[i];
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+        const uint32_t row = (w * LB + i) * 8 + (lane >> 3), in = n0 + row < p.n ? row : p.n - 1 - n0;
+        cb[i] = ((lane & 7u) ^ key_b(row)) * 16;
+        vb[i] = in * p.b_stride + cb[i];
+    }
+    // one of this wave's copies of 8 rows; past the last step: zeros
+    const auto copy_a = [&](uint32_t s, uint8_t *as, int i) {
+        const uint32_t k0 = s * kStep, v = KTAIL && k0 + ca[i] >= p.k ? kOutside : va[i];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(pa, s < s1 ? kInside : 0),
+                                                 (lds_void *)(as + (w * LA + i) * 1024), 16, v, k0, 0, 0);
+    };
+    const auto copy_b = [&](uint32_t s, uint8_t *bs, int i) {
+        const uint32_t k0 = s * kStep, v = KTAIL && k0 + cb[i] >= p.k ? kOutside : vb[i];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(pb, s < s1 ? kInside : 0),
+                                                 (lds_void *)(bs + (w * LB + i) * 1024), 16, v, k0, 0, 0);
+    };
+    // k ends inside a chunk: its bytes past k, which may hold anything, are
+    // cleared in LDS
+    const auto clear_tail = [&](uint8_t *as, uint8_t *bs) {
+        const uint32_t chunk = (p.k % kStep) / 16, keep = p.k % 16;
+        for (uint32_t row = threadIdx.x; row < BM + BN; row += 256) {
+            uint8_t *const at = row < BM ? as + row * kStep + (chunk ^ key_a(row)) * 16
+                                         : bs + (row - BM) * kStep + (chunk ^ key_b(row - BM)) * 16;
+            for (uint32_t e = keep; e < 16; ++e) at[e] = 0;
+        }
+        __syncthreads();
+    };
+    const bool partial_chunk = KTAIL && p.k % 16 != 0 && s1 == all_steps;
+
+    const uint32_t row_b = wn * 64 + 32 * ((r >> 2) & 1u) + 8 * (r >> 3) + (r & 3u);
+    const uint32_t oa = (wm * 128 + r) * kStep + (g ^ key_a(r)) * 16;
+    const uint32_t ob = row_b * kStep + (g ^ key_b(row_b)) * 16;
+    const auto read_a = [&](const uint8_t *as, int i) {
+        Raw x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x.c[j] = *reinterpret_cast<const i32x4 *>(as + (oa ^ (32u * j)) + i * 32 * kStep);
+        return x;
+    };
+    const auto read_b = [&](const uint8_t *bs, int f) {
+        Raw x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x.c[j] = *reinterpret_cast<const i32x4 *>(bs + (ob ^ (32u * j)) + f * 4 * kStep);
+        return x;
+    };
+    // scales: a dword has a row's bytes for four steps
+    constexpr int NB = BLOCKS ? 1 : 2;
+    const uint8_t *const qa = p.a_scale + (uint64_t)m0 * p.a_scale_stride;
+    const uint8_t *const qb = p.b_scale + (uint64_t)(BLOCKS ? n0 / 128 : n0) * p.b_scale_stride;
+    uint32_t va_scale[4], vb_scale[NB];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = wm * 128 + i * 32 + r;
+        va_scale[i] = (m0 + row < p.m ? row : p.m - 1 - m0) * p.a_scale_stride;
+    }
+#pragma unroll
+    for (int f = 0; f < NB; ++f) {
+        const uint32_t row = row_b + 4 * f;
+        vb_scale[f] = BLOCKS ? 0 : (n0 + row < p.n ? row : p.n - 1 - n0) * p.b_scale_stride;  // n0 is a multiple of 128
+    }
+    int sa[4], sb[NB], ha[4], hb[NB], na[4], nb[NB];  // this pair of steps', these four steps', the next four's
+    int pa_next[4], pb_next[NB];                      // the next pair of steps'
+    const auto load_scales = [&](uint32_t s, int *ta, int *tb) {
+        const uint32_t at = s < s1 ? s : s0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ta[i] = *reinterpret_cast<const int *>(qa + at + va_scale[i]);
+#pragma unroll
+        for (int f = 0; f < NB; ++f) tb[f] = *reinterpret_cast<const int *>(qb + at + vb_scale[f]);
+    };
+
+    f32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) acc[i][f] = (f32x16)0.0f;
+    Wide64 aw, an_wide, bw[2];  // this fragment of A, the next one, B's
+    Raw raw;                    // the fragment of A after aw
+
+    // step s, whose operands are in (as, bs) and the next one's in (an, bn)
+    const auto step = [&](auto par, uint32_t s, uint8_t *as, uint8_t *bs, uint8_t *an, uint8_t *bn) {
+        constexpr int S = decltype(par)::value;
+#pragma unroll
+        for (int ag = 0; ag < 4; ++ag) {
+            Raw after, rb[2];
+            float scale_a, scale_b[2];
+            if (ag < 3) {
+                if (ag < 2) after = read_a(as, ag + 2);
+                scale_a = scale_of<S>(sa[(ag + 1) & 3]);
+            } else {
+                // this wave's LDS reads are done, and its copies but the last
+                // LB, of B's step after the next
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LB) : "memory");
+                if (partial_chunk && s + 2 == s1) clear_tail(an, bn);
+                raw = read_a(an, 0);
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    rb[f] = read_b(bn, f);
+                    scale_b[f] = S == 0 ? scale_of<1>(sb[BLOCKS ? 0 : f]) : scale_of<0>(pb_next[BLOCKS ? 0 : f]);
+                }
+                after = read_a(an, 1);
+                scale_a = S == 0 ? scale_of<1>(sa[0]) : scale_of<0>(pa_next[0]);
+            }
+            // every wave holds its part of B: its place is free
+            if (ag == 1) asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                // a copy before every fourth product, B's every eighth
+                if (k % 2 == 0) {
+                    if (ag == 3) copy_a(s + 2, as, k / 2);
+                    else if (ag == 0) copy_a(s + 1, an, LA / 2 + k / 2);
+                    else if (k % 4 == 0) copy_b(s + 2, bs, (ag - 1) * (LB / 2) + k / 4);
+                }
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    acc[ag][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[f].v[k], aw.v[k], acc[ag][f], 0, 0, 0);
+                // (in the last group two places late: the reads take that long)
+                const int late = ag == 3 ? 2 : 0;
+                if (k >= late) {
+                    an_wide.v[k - late] = widen_piece(raw, k - late, scale_a);
+                    if (ag == 3) {
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) bw[f].v[k - late] = widen_piece(rb[f], k - late, scale_b[f]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (ag == 3) {
+#pragma unroll
+                for (int k = 6; k < 8; ++k) {
+                    an_wide.v[k] = widen_piece(raw, k, scale_a);
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) bw[f].v[k] = widen_piece(rb[f], k, scale_b[f]);
+                }
+            }
+            aw = an_wide;
+            raw = after;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) asm volatile("" : "+a"(acc[ag][f]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    load_scales(s0, ha, hb);
+#pragma unroll
+    for (int i = 0; i < LA; ++i) copy_a(s0, as0, i);
+#pragma unroll
+    for (int i = 0; i < LB; ++i) copy_b(s0, bs0, i);
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __syncthreads();
+    if (partial_chunk && s0 + 1 == s1) clear_tail(as0, bs0);
+#pragma unroll
+    for (int i = 0; i < LB; ++i) copy_b(s0 + 1, bs1, i);
+#pragma unroll
+    for (int i = 0; i < LA / 2; ++i) copy_a(s0 + 1, as1, i);
+    {
+        const Raw x = read_a(as0, 0), y[2] = {read_b(bs0, 0), read_b(bs0, 1)};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            aw.v[k] = widen_piece(x, k, scale_of<0>(ha[0]));
+#pragma unroll
+            for (int f = 0; f < 2; ++f) bw[f].v[k] = widen_piece(y[f], k, scale_of<0>(hb[BLOCKS ? 0 : f]));
+        }
+        raw = read_a(as0, 1);
+    }
+    // two steps a turn, the second of an odd number on zeros; s0 is a multiple of 4
+    uint32_t s = s0;
+    do {
+        if ((s & 2u) == 0) load_scales(s + 4, na, nb);
+        // a step past k's end has no scale: 1 in place of what stands there
+        const uint32_t shift = (s & 2u) * 8;
+        const int keep = s + 1 < all_steps ? -1 : 0xFF, fill = s + 1 < all_steps ? 0 : 0x7F00;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sa[i] = ((ha[i] >> shift) & keep) | fill;
+            pa_next[i] = (s & 2u) ? na[i] : ha[i] >> 16;
+        }
+#pragma unroll
+        for (int f = 0; f < NB; ++f) {
+            sb[f] = ((hb[f] >> shift) & keep) | fill;
+            pb_next[f] = (s & 2u) ? nb[f] : hb[f] >> 16;
+        }
+        step(std::integral_constant<int, 0>{}, s, as0, bs0, as1, bs1);
+        step(std::integral_constant<int, 1>{}, s + 1, as1, bs1, as0, bs0);
+        if (s & 2u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ha[i] = na[i];
+#pragma unroll
+            for (int f = 0; f < NB; ++f) hb[f] = nb[f];
+        }
+        s += 2;
+    } while (s < s1);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // the copies past the end (zeros) are in LDS while it is this workgroup's
+
+    float *const out = (float *)p.out + at.split * p.split_stride;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = m0 + wm * 128 + i * 32 + r;
+        if (row >= p.m) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = acc[i][e >> 2][4 * q + (e & 3)];
+            put_out(out, kF32, row, p.out_stride, n0 + wn * 64 + 32 * g + 8 * q, p.n, o);
         }
     }
 }
@@ -657,8 +938,8 @@ Cut cut_of(uint64_t m, uint64_t n, uint64_t k, bool exact)
     // per workgroup, and the pass that joins splits
     double least = 0;
     struct Kind { int fm, fn; double step, ends; uint32_t per_cu; };
-    static const Kind narrow[] = {{8, 8, 2700, 6000, 1}, {4, 4, 900, 4000, 2}, {2, 2, 330, 3000, 4}};
-    static const Kind wide[] = {{8, 4, 2600, 6000, 1}, {4, 4, 1800, 4000, 2}, {2, 2, 660, 3000, 4}};
+    static const Kind narrow[] = {{8, 8, 2430, 6000, 1}, {4, 4, 900, 4000, 2}, {2, 2, 330, 3000, 4}};
+    static const Kind wide[] = {{8, 4, 2280, 6000, 1}, {4, 4, 1800, 4000, 2}, {2, 2, 660, 3000, 4}};
     const Kind *const kinds = exact ? wide : narrow;
     for (int q = 0; q < 3; ++q) {
         const Kind &t = kinds[q];
@@ -738,7 +1019,10 @@ hipError_t launch_gemm(const GemmArgs &g)
     const uint32_t blocks = p.tiles_m * p.tiles_n * c.splits;
     if (c.fm == 4) launch_tile<4, 4, BLOCKS, EXACT>(p, blocks, g.stream);
     else if (c.fm == 2) launch_tile<2, 2, BLOCKS, EXACT>(p, blocks, g.stream);
-    else launch_tile<8, EXACT ? 4 : 8, BLOCKS, EXACT>(p, blocks, g.stream);  // wide operands leave room for half
+    else if constexpr (EXACT) {
+        if (p.k % kStep) gemm_wide<BLOCKS, true><<<blocks, 256, 0, g.stream>>>(p);
+        else gemm_wide<BLOCKS, false><<<blocks, 256, 0, g.stream>>>(p);
+    } else launch_tile<8, 8, BLOCKS, false>(p, blocks, g.stream);
     if (c.splits > 1) {
         const uint64_t n8 = div_up(g.n, 8), count = g.m * n8;
         const uint64_t wgs = div_up(count, 256);
