@@ -102,7 +102,8 @@ class EmbedPlan(NamedTuple):
 
 def embed_plan(ids, rows: int, stream=None) -> EmbedPlan:
     """Groups ids by row for embed_grad; ids outside [0, rows) take no part."""
-    return EmbedPlan(ids.shape[0], rows, *_torch.embed_plan(ids, rows, stream))
+    made = _torch.embed_plan(ids, rows, stream)
+    return EmbedPlan(made[0].shape[0], rows, *made)
 
 
 def embed_grad(plan: EmbedPlan, dout, scale: float = 1.0, stream=None):
