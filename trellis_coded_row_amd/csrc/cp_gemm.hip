@@ -13,7 +13,13 @@
 // 32-bit outputs are not to lose that, so there each value times its scale
 // is converted to bf16 (e4m3 has 4 significant bits: exact) on the way from
 // LDS to the bf16 matrix instruction (measured: 1e-8 to 2e-7 of the result's
-// rms, the 32-bit sum's own rounding), at half the rate.
+// rms, the 32-bit sum's own rounding), at half the rate and with the
+// conversions beside it.
+//
+// Reached: 4,096 x 4,096 x 24,576 to bf16 in 308 us, 2.68 PFLOP/s (the vendor
+// library's product with one scale for each operand: 303 us); 4,096 x 24,576 x
+// 4,096 to 32 bits in 800 us, 1.03 PFLOP/s (its bf16 product, with a 16-bit
+// output: 652 us); 8 x 4,096 x 24,576 in 22.6 us, 4.5 TB/s (a copy: 5.0).
 //
 // The operands are passed swapped (B's rows as the instruction's rows), so
 // that a lane's four results are neighbours in an output row.
@@ -169,6 +175,14 @@ __device__ __forceinline__ TilePlace place_of(const TileParams &p, uint32_t BM, 
 // own copies of the next have landed, so the first fragments of the next
 // step are read, and the copies of the step after it start, under those
 // products.
+//
+// SPREAD, for the largest tile: a compute unit takes in about 32 bytes of
+// copies per cycle, so that a step's 64 KiB last as long as its products (32
+// cycles each, 64 of them per wave) and are issued over all of it. A's go
+// into the buffer that the barrier has freed, half of them in the next step's
+// first group; B's a step earlier, behind a second barrier after the first
+// group, when every wave holds its fragments of B. Issued together in the
+// last group they took 2,160 cycles there, and a step 3,790.
 //
 // LDS: a row's 128 bytes are 8 chunks of 16; chunk c of the fragment row r
 // stands at c ^ (r / 2). A 16-byte LDS read serves 16 lanes at a time, 8 of
@@ -509,8 +523,10 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
 }
 
 // 32-bit outputs of large matrices: tiles of 256 x 128 as above, with the
-// 32 x 32 bf16 instruction (measured on one unit: 1,011 operations per cycle,
-// the 16 x 16 one 600). Four waves, 2 x 2, each with 4 x 2 fragments of
+// 32 x 32 bf16 instruction (measured on one SIMD unit: 1,011 operations per
+// cycle, the 16 x 16 one 600; the product below went from 927 to 811 us). Bound
+// by the issue of a wave's products and conversions, 64 and 192 a step, which
+// take turns. Four waves, 2 x 2, each with 4 x 2 fragments of
 // 32 x 32: lane l carries row l % 32 and the 16-byte chunks l / 32 + 2 j
 // (j < 4) of its 128 values. A step goes by A's fragments, 16 products each;
 // the next fragment is widened, and the one after it read, under them.
