@@ -524,9 +524,10 @@ __global__ __launch_bounds__(256) void gemm_tile(TileParams p)
 
 // 32-bit outputs of large matrices: tiles of 256 x 128 as above, with the
 // 32 x 32 bf16 instruction (measured on one SIMD unit: 1,011 operations per
-// cycle, the 16 x 16 one 600; the product below went from 927 to 811 us). Bound
-// by the issue of a wave's products and conversions, 64 and 192 a step, which
-// take turns. Four waves, 2 x 2, each with 4 x 2 fragments of
+// cycle, the 16 x 16 one 600; the product above went from 927 to 811 us). Bound
+// by a wave's issue: alone on its unit it issues a vector instruction every 8
+// cycles (measured), so that a step's 192 conversions take 1,600 cycles beside
+// 64 products of 32. Four waves, 2 x 2, each with 4 x 2 fragments of
 // 32 x 32: lane l carries row l % 32 and the 16-byte chunks l / 32 + 2 j
 // (j < 4) of its 128 values. A step goes by A's fragments, 16 products each;
 // the next fragment is widened, and the one after it read, under them.
