@@ -6,8 +6,12 @@
 //
 // Bound by memory: the matrix is read once, in tiles of 128 x 128 that hold
 // whole groups of both directions, and both outputs are written from it.
-// 4,096 x 24,576 bf16 in blocks, both ways: 88 us, 4.6 TB/s (a copy: 5.0). 1,000 x
-// 2,050 (136 tiles, fewer than compute units): 9.8 us, a tile's latency.
+// 4,096 x 24,576 bf16 in blocks, both ways: 87 us, 4.6 TB/s (a copy: 5.0). 1,000 x
+// 2,050 (136 tiles, fewer than compute units): 8.3 us, a tile's latency: a wave
+// alone on its SIMD unit issues slowly, so values are tested for what is not
+// finite by their maxima, not one by one (which took 9.8).
+#include <type_traits>
+
 #include "cp_ops_internal.h"
 
 namespace cpk {
@@ -54,19 +58,46 @@ __global__ __launch_bounds__(256) void quantize_tile(const typename Elem<DT>::ra
         if (r0 + i < n) v[i] = load8<DT>(x + (r0 + i) * x_stride, c0, d);
         else v[i] = (typename Elem<DT>::raw)0;
     }
-    // largest magnitudes: of each row's 8 columns and each column's 8 rows
+    // largest magnitudes: of each row's 8 columns and each column's 8 rows.
+    // Where one of the thread's values is not finite, which its maxima then
+    // are not either, it takes them again among those that are.
     uint32_t mr[8], mc[8];
+    float fr[8], fc[8], most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mr[i] = mc[i] = 0;
+    for (int i = 0; i < 8; ++i) fr[i] = fc[i] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint32_t b = finite_bits(Elem<DT>::get(v[i][e]));
-            mr[i] = mr[i] > b ? mr[i] : b;
-            if constexpr (TRANS && !BLOCKS) mc[e] = mc[e] > b ? mc[e] : b;
+            const float f = __builtin_fabsf(Elem<DT>::get(v[i][e]));
+            fr[i] = __builtin_elementwise_maximum(fr[i], f);
+            if constexpr (TRANS && !BLOCKS) fc[e] = __builtin_elementwise_maximum(fc[e], f);
         }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        most = __builtin_elementwise_maximum(most, fr[i]);
+        mr[i] = __float_as_uint(fr[i]);
+        mc[i] = __float_as_uint(fc[i]);
+    }
+    const bool odd = !(most < __builtin_inff());
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mr[i] = mc[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t b = finite_bits(Elem<DT>::get(v[i][e]));
+                mr[i] = mr[i] > b ? mr[i] : b;
+                mc[e] = mc[e] > b ? mc[e] : b;
+            }
+        }
+    }
+    const auto four = [](auto check, float a, float b, float c, float d, float inv) {
+        if constexpr (decltype(check)::value) return to_e4m3x4(a, b, c, d, inv);
+        else return finite_to_e4m3x4(a, b, c, d, inv);
+    };
     uint32_t byte_r[8], byte_c[8];
     if constexpr (BLOCKS) {
         uint32_t m = 0;
@@ -117,29 +148,35 @@ __global__ __launch_bounds__(256) void quantize_tile(const typename Elem<DT>::ra
         }
     }
     const uint32_t left = c0 < d ? d - c0 : 0;
+    const auto convert = [&](auto check) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float inv = inverse_scale(byte_r[BLOCKS ? 0 : i]);
-        u32x2 o;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            o[h] = to_e4m3x4(Elem<DT>::get(v[i][4 * h]), Elem<DT>::get(v[i][4 * h + 1]),
-                             Elem<DT>::get(v[i][4 * h + 2]), Elem<DT>::get(v[i][4 * h + 3]), inv);
-        if (r0 + i < n) put8(q + (r0 + i) * q_stride + c0, o, left);
-    }
-    if constexpr (TRANS) {
-        // column e's 8 rows: piece rl / 8 of LDS row cl + e
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float inv = inverse_scale(BLOCKS ? byte_r[0] : byte_c[e]);
+        for (int i = 0; i < 8; ++i) {
+            const float inv = inverse_scale(byte_r[BLOCKS ? 0 : i]);
             u32x2 o;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                o[h] = to_e4m3x4(Elem<DT>::get(v[4 * h][e]), Elem<DT>::get(v[4 * h + 1][e]),
-                                 Elem<DT>::get(v[4 * h + 2][e]), Elem<DT>::get(v[4 * h + 3][e]), inv);
-            const uint32_t piece = (rl >> 3) ^ (cl >> 3);
-            *reinterpret_cast<u32x2 *>(lds + (cl + e) * kTile + piece * 8u) = o;
+                o[h] = four(check, Elem<DT>::get(v[i][4 * h]), Elem<DT>::get(v[i][4 * h + 1]),
+                            Elem<DT>::get(v[i][4 * h + 2]), Elem<DT>::get(v[i][4 * h + 3]), inv);
+            if (r0 + i < n) put8(q + (r0 + i) * q_stride + c0, o, left);
         }
+        if constexpr (TRANS) {
+            // column e's 8 rows: piece rl / 8 of LDS row cl + e
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float inv = inverse_scale(BLOCKS ? byte_r[0] : byte_c[e]);
+                u32x2 o;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    o[h] = four(check, Elem<DT>::get(v[4 * h][e]), Elem<DT>::get(v[4 * h + 1][e]),
+                                Elem<DT>::get(v[4 * h + 2][e]), Elem<DT>::get(v[4 * h + 3][e]), inv);
+                const uint32_t piece = (rl >> 3) ^ (cl >> 3);
+                *reinterpret_cast<u32x2 *>(lds + (cl + e) * kTile + piece * 8u) = o;
+            }
+        }
+    };
+    if (odd) convert(std::true_type{});
+    else convert(std::false_type{});
+    if constexpr (TRANS) {
         __syncthreads();
         // 8 lanes write an output row's 128 bytes, 16 at a time
 #pragma unroll
