@@ -47,3 +47,10 @@ def test_wrong_tensors_on_the_gpu():
     outs = [cp.embed_lookup(x, ids, stream=s) for s in (None, side, side.cuda_stream, 0)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_the_gradient_of_too_long_rows_is_not_supported():
+    p = 1 << 20  # a stand-in address, never dereferenced
+    f = lambda d: cp.cp_embed_grad(p, p, p, p, p, 4, 10, p, cp.CP_DTYPE_F32, d, d, 1.0, p, p, 1 << 40, None)
+    assert f(2**21 + 1) == cp.CP_ERR_UNSUPPORTED and f(2**31) == cp.CP_ERR_INVALID_ARGUMENT
+    assert cp.cp_embed_grad_workspace_bytes(4, 2**21 + 1) == 0 and cp.cp_embed_grad_workspace_bytes(4, 2**21) > 0
