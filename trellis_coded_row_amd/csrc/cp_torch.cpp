@@ -95,19 +95,26 @@ at::Tensor empty(c10::IntArrayRef sizes, at::ScalarType type, c10::Device device
     return at::Tensor(at::detail::empty_cuda(sizes, type, device, std::nullopt));
 }
 
-// rows x cols bytes whose rows start on `unit` bytes and end on them.
-at::Tensor empty_bytes(int64_t rows, int64_t cols, int64_t unit, at::ScalarType type, c10::Device device)
+// An 8-bit matrix and its scales: rows x cols of e4m3 whose rows start on 16
+// bytes and srows x scols of e8m0 whose rows start on 4, each row readable up
+// to there. They are used and dropped together, so they share an allocation
+// (one takes about 0.9 us of a call of 7).
+struct EightBits {
+    at::Tensor q, scale;
+};
+
+EightBits empty_eight_bits(int64_t rows, int64_t cols, int64_t srows, int64_t scols, c10::Device device)
 {
-    const int64_t wide = up(cols, unit);
-    at::Tensor t = empty({rows, wide}, type, device);
-    if (wide != cols) t.unsafeGetTensorImpl()->set_sizes_and_strides(c10::IntArrayRef{rows, cols},
-                                                                          c10::IntArrayRef{wide, 1});
+    const int64_t wide = up(cols, 16), swide = up(scols, 4), first = up(rows * wide, 256);
+    EightBits t;
+    t.q = empty({first + srows * swide}, kE4m3, device);
+    t.scale = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.q.storage()), t.q.key_set(),
+                                                       c10::scalarTypeToTypeMeta(kE8m0));
+    t.scale.unsafeGetTensorImpl()->set_storage_offset(first);
+    t.scale.unsafeGetTensorImpl()->set_sizes_and_strides(c10::IntArrayRef{srows, scols}, c10::IntArrayRef{swide, 1});
+    t.q.unsafeGetTensorImpl()->set_sizes_and_strides(c10::IntArrayRef{rows, cols}, c10::IntArrayRef{wide, 1});
     return t;
 }
-
-at::Tensor empty_e4m3(int64_t rows, int64_t cols, c10::Device device) { return empty_bytes(rows, cols, 16, kE4m3, device); }
-
-at::Tensor empty_e8m0(int64_t rows, int64_t cols, c10::Device device) { return empty_bytes(rows, cols, 4, kE8m0, device); }
 
 void *ptr(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 
@@ -367,8 +374,9 @@ PyObject *rms_norm(PyObject *, PyObject *const *arg, Py_ssize_t count)
     }
     if (truth(arg[4])) y = empty({n, d}, type, device);
     if (eight) {
-        q = empty_e4m3(n, d, device);
-        scale = empty_e8m0(n, groups_of(d), device);
+        EightBits t = empty_eight_bits(n, d, n, groups_of(d), device);
+        q = std::move(t.q);
+        scale = std::move(t.scale);
     }
     if (truth(arg[6])) rstd = empty({n}, at::ScalarType::Float, device);
     for (const at::Tensor &t : {y, q, scale, rstd}) stream.keep(t);
@@ -426,11 +434,13 @@ PyObject *quantize_fp8(PyObject *, PyObject *const *arg, Py_ssize_t count)
     const c10::Device device = x.device();
     const bool blocks = truth(arg[1]), both = truth(arg[2]);
     const Stream stream(arg[3], device);
-    const at::Tensor q = empty_e4m3(n, d, device), scale = empty_e8m0(blocks ? gn : n, gd, device);
+    const EightBits t = empty_eight_bits(n, d, blocks ? gn : n, gd, device);
+    const at::Tensor &q = t.q, &scale = t.scale;
     at::Tensor qt, scale_t;
     if (both) {
-        qt = empty_e4m3(d, n, device);
-        scale_t = empty_e8m0(blocks ? gd : d, gn, device);
+        EightBits other = empty_eight_bits(d, n, blocks ? gd : d, gn, device);
+        qt = std::move(other.q);
+        scale_t = std::move(other.scale);
     }
     for (const at::Tensor &t : {q, scale, qt, scale_t}) stream.keep(t);
     if (n && d)

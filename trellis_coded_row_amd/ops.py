@@ -17,7 +17,7 @@ the calls of a single token's step take no longer than their host side.
 
 8-bit matrices are ``torch.float8_e4m3fn`` with ``torch.float8_e8m0fnu``
 scales. Those made here have rows that start on 16 bytes (4 for scales), as
-``gemm_fp8`` needs them.
+``gemm_fp8`` needs them; a matrix and its scales share one allocation.
 """
 from __future__ import annotations
 
