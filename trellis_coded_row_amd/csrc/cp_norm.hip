@@ -30,31 +30,6 @@ __device__ __forceinline__ float row_sum(float v, float *part)
     return v;
 }
 
-// 1 / sqrt(v) as a sum hi + lo, lo below hi's last bit: the instruction is off
-// by up to one in the last bit, which a Newton step takes away.
-struct Root {
-    float hi, lo;
-};
-
-__device__ __forceinline__ Root inverse_root(float v)
-{
-    const float r = rsqrtf(v), t = v * r;
-    if (!(r > 0.0f && r < __builtin_inff())) return {r, 0.0f};
-    const float under = fmaf(v, r, -t);              // v r = t + under
-    const float e = fmaf(-t, r, 1.0f) - under * r;   // 1 - v r^2
-    const float step = 0.5f * r * e, hi = r + step;
-    return {hi, step - (hi - r)};
-}
-
-// h * rstd * w rounded once, for values that are rounded to e4m3 next: with
-// each product rounded by itself, more of them change sides at a border
-// between two e4m3 values. Not finite where the plain product is not.
-__device__ __forceinline__ float normed(float h, Root r, float w)
-{
-    const float p = h * r.hi;
-    return fmaf(p, w, fmaf(h, r.lo, fmaf(h, r.hi, -p)) * w);
-}
-
 // The 8-bit outputs of columns [c, c + 8) (y zero past the row's end); the
 // 16 lanes of a row of lanes hold one group of 128.
 __device__ __forceinline__ void put_group(const float *y, uint32_t c, uint32_t d, uint8_t *q, uint8_t *scale)
@@ -103,7 +78,7 @@ constexpr uint32_t kAheadWaves = 4096;  // waves that stay: four for each SIMD u
 // W waves per row, IT chunks of 8 columns per lane: chunk i of a lane is
 // columns 8 (64 W i + lane of the row).
 //
-// Bound by memory: 4,096 bf16 rows of 24,576 to 8 bits take 65 us, 4.65 TB/s (a
+// Bound by memory: 4,096 bf16 rows of 24,576 to 8 bits take 63 us, 4.8 TB/s (a
 // copy reaches 5.0). With one row per workgroup, none read ahead, 73 us: then
 // a workgroup's loads, its barrier and its stores follow one another.
 template <int DT, int W, int IT, bool RES>
@@ -153,8 +128,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_rows(
         }
         sum = row_sum<W>(sum, part[flip]);  // two places in turn: a barrier a row
         flip ^= 1;
-        const Root rstd = inverse_root(sum / (float)d + eps);
-        if (rstd_out && lane == 0) rstd_out[row] = rstd.hi;
+        const float rstd = rsqrtf(sum / (float)d + eps);
+        if (rstd_out && lane == 0) rstd_out[row] = rstd;
         // from here the values are made from x and the residual again: kept,
         // they would take twice the registers
 #pragma unroll
@@ -174,17 +149,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_rows(
                 if (h_out && c < d) store8<DT>(h_out + (uint64_t)row * d, c, d, h);
             }
             if (!AHEAD && (y_out || q)) vw[i] = load8<DT>(weight, c, d);
+            if (!y_out && !q) continue;
+            // (past the row's end, h and the weight are zero. Of 100 million
+            // 8-bit values some 50 lie so near a border that they fall on its
+            // other side than in 64 bits: as many with the product rounded
+            // once from a root in 64 bits, at 3 us more for them)
             float y[8];
-            if (y_out && c < d) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = value(i, e) * rstd.hi * Elem<DT>::get(vw[i][e]);
-                store8<DT>(y_out + (uint64_t)row * d, c, d, y);
-            }
-            if (q) {  // past the row's end, h and the weight are zero
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = normed(value(i, e), rstd, Elem<DT>::get(vw[i][e]));
-                put_group(y, c, d, q + row * q_stride, q_scale + row * scale_stride);
-            }
+            for (int e = 0; e < 8; ++e) y[e] = value(i, e) * rstd * Elem<DT>::get(vw[i][e]);
+            if (y_out && c < d) store8<DT>(y_out + (uint64_t)row * d, c, d, y);
+            if (q) put_group(y, c, d, q + row * q_stride, q_scale + row * scale_stride);
         }
         if constexpr (AHEAD) {
 #pragma unroll
@@ -210,7 +184,7 @@ __global__ __launch_bounds__(kLongWaves * 64) void norm_long(
     __shared__ float part[kLongWaves];
     const uint64_t row = blockIdx.x;
     const uint32_t step = kLongWaves * 64u * 8u;
-    Root rstd{};
+    float rstd = 0.0f;
     for (int pass = 0; pass < 2; ++pass) {
         float sum = 0.0f;
         for (uint32_t c0 = 0; c0 < d; c0 += step) {  // all lanes, for put_group's maximum
@@ -231,22 +205,16 @@ __global__ __launch_bounds__(kLongWaves * 64) void norm_long(
                 if (h_out && c < d) store8<DT>(h_out + row * d, c, d, h);
                 const typename Elem<DT>::vec8 w = load8<DT>(weight, c, d);
                 float y[8];
-                if (y_out && c < d) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = h[e] * rstd.hi * Elem<DT>::get(w[e]);
-                    store8<DT>(y_out + row * d, c, d, y);
-                }
-                if (q) {  // past the row's end, h and the weight are zero
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = normed(h[e], rstd, Elem<DT>::get(w[e]));
-                    put_group(y, c, d, q + row * q_stride, q_scale + row * scale_stride);
-                }
+                for (int e = 0; e < 8; ++e) y[e] = h[e] * rstd * Elem<DT>::get(w[e]);
+                if (y_out && c < d) store8<DT>(y_out + row * d, c, d, y);
+                if (q) put_group(y, c, d, q + row * q_stride, q_scale + row * scale_stride);
             }
         }
         if (pass == 0) {
             sum = row_sum<kLongWaves>(sum, part);
-            rstd = inverse_root(sum / (float)d + eps);
-            if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd.hi;
+            rstd = rsqrtf(sum / (float)d + eps);
+            if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
         }
     }
 }
