@@ -26,8 +26,7 @@ namespace {
 constexpr int64_t kGroup = 128;  // values that share a scale
 constexpr auto kE4m3 = at::ScalarType::Float8_e4m3fn, kE8m0 = at::ScalarType::Float8_e8m0fnu;
 
-PyObject *cp_error = nullptr;         // CPError(status, name)
-PyObject *keep_for_stream = nullptr;  // (tensor, stream): its memory is not handed out before that work is done
+PyObject *cp_error = nullptr;  // CPError(status, name)
 
 int64_t up(int64_t v, int64_t unit) { return (v + unit - 1) / unit * unit; }
 
@@ -124,16 +123,47 @@ T *ptr(const at::Tensor &t)
     return static_cast<T *>(ptr(t));
 }
 
-// The stream of a call. Tensors made for work on a stream other than
-// torch's current one are made known to torch's allocator.
+// The stream of a call, torch's current one while this lives: what is made for
+// the call comes from that stream's memory. A block that the caller's own
+// current stream gave back may still be read there by work that the call's
+// stream does not wait for. An output that the call returns is also made known
+// to the allocator as used by the caller's stream (keep), so that dropping it
+// there does not hand its memory to the call's stream too early.
 class Stream {
   public:
-    Stream(PyObject *o, c10::Device device) : o_(o)
+    Stream(PyObject *o, c10::Device device) : before_(c10::hip::getCurrentHIPStream(device.index()))
     {
-        if (o == Py_None) {
-            handle_ = c10::hip::getCurrentHIPStream(device.index()).stream();
-            return;
-        }
+        handle_ = o == Py_None ? before_.stream() : static_cast<hipStream_t>(handle_of(o));
+        other_ = handle_ != before_.stream();
+        if (other_)
+            c10::hip::setCurrentHIPStream(handle_ ? c10::hip::getStreamFromExternal(handle_, device.index())
+                                                  : c10::hip::getDefaultHIPStream(device.index()));
+    }
+
+    ~Stream()
+    {
+        if (other_) c10::hip::setCurrentHIPStream(before_);
+    }
+
+    Stream(const Stream &) = delete;
+    Stream &operator=(const Stream &) = delete;
+
+    void *handle() const { return handle_; }
+
+    void keep(const at::Tensor &t) const
+    {
+        // (torch names this device type cuda on tensors, hip in its HIPStream)
+        if (other_ && t.defined()) t.record_stream(c10::Stream(c10::Stream::UNSAFE, t.device(), before_.id()));
+    }
+
+    at::Tensor workspace(uint64_t bytes, c10::Device device) const
+    {
+        return bytes ? empty({(int64_t)bytes}, at::ScalarType::Byte, device) : at::Tensor();
+    }
+
+  private:
+    static void *handle_of(PyObject *o)
+    {
         PyObject *const of = PyObject_GetAttrString(o, "cuda_stream");
         if (!of) {
             if (!PyErr_ExceptionMatches(PyExc_AttributeError)) throw python_error();
@@ -142,37 +172,15 @@ class Stream {
         PyObject *const number = PyNumber_Long(of ? of : o);
         Py_XDECREF(of);
         if (!number) throw python_error();
-        handle_ = PyLong_AsVoidPtr(number);
+        void *const handle = PyLong_AsVoidPtr(number);
         Py_DECREF(number);
-        if (!handle_ && PyErr_Occurred()) throw python_error();
+        if (!handle && PyErr_Occurred()) throw python_error();
+        return handle;
     }
 
-    void *handle() const { return handle_; }
-
-    void keep(const at::Tensor &t) const
-    {
-        if (o_ == Py_None || !t.defined()) return;
-        PyObject *const w = THPVariable_Wrap(t);
-        if (!w) throw python_error();
-        PyObject *const r = PyObject_CallFunctionObjArgs(keep_for_stream, w, o_, nullptr);
-        Py_DECREF(w);
-        if (!r) throw python_error();
-        Py_DECREF(r);
-    }
-
-    at::Tensor workspace(uint64_t bytes, c10::Device device) const
-    {
-        at::Tensor t;
-        if (bytes) {
-            t = empty({(int64_t)bytes}, at::ScalarType::Byte, device);
-            keep(t);
-        }
-        return t;
-    }
-
-  private:
-    PyObject *o_;
-    void *handle_ = nullptr;
+    c10::hip::HIPStream before_;
+    hipStream_t handle_ = nullptr;
+    bool other_ = false;
 };
 
 // A C call with `device` current; CPError for a status other than CP_OK.
@@ -516,17 +524,14 @@ PyObject *gemm_fp8(PyObject *, PyObject *const *arg, Py_ssize_t count)
     END_HANDLE_TH_ERRORS
 }
 
-// (CPError, function): see cp_error, keep_for_stream.
+// (CPError): see cp_error.
 PyObject *setup(PyObject *, PyObject *const *arg, Py_ssize_t count)
 {
     HANDLE_TH_ERRORS
-    arguments(count, 2);
+    arguments(count, 1);
     Py_INCREF(arg[0]);
-    Py_INCREF(arg[1]);
     Py_XDECREF(cp_error);
-    Py_XDECREF(keep_for_stream);
     cp_error = arg[0];
-    keep_for_stream = arg[1];
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }

@@ -11,9 +11,14 @@ arithmetic runs in the library's HIP kernels. The functions named ``cp_*``
 are the C entry points themselves (raw pointers and integers, a status
 returned); the others take torch tensors on one GPU, allocate their outputs,
 and raise ``ValueError`` for tensors they do not take and ``CPError`` for a
-status other than CP_OK. ``stream=None`` is torch's current stream. Their
-checks, outputs and workspaces are made in C++ (``csrc/cp_torch.cpp``), as
-the calls of a single token's step take no longer than their host side.
+status other than CP_OK. Their checks, outputs and workspaces are made in C++
+(``csrc/cp_torch.cpp``), as the calls of a single token's step take no longer
+than their host side.
+
+``stream=None`` is torch's current stream. A call on another one (a stream or
+its handle) does not wait for the current one: its inputs have to be ready
+there and stay alive until it is done. What it allocates comes from that
+stream's memory; an output may be dropped on the current stream after use there.
 
 8-bit matrices are ``torch.float8_e4m3fn`` with ``torch.float8_e8m0fnu``
 scales. Those made here have rows that start on 16 bytes (4 for scales), as
@@ -26,7 +31,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import CPError, _L, _keep_for_stream, library_path
+from . import CPError, _L, library_path
 from . import _cp_torch as _torch
 
 __all__ = [
@@ -72,7 +77,7 @@ cp_gemm_fp8 = _bind("cp_gemm_fp8", _int, _vp, _u64, _vp, _u64, _vp, _u64, _vp, _
                     _int, _vp, _u64, _vp)
 
 
-_torch.setup(CPError, _keep_for_stream)
+_torch.setup(CPError)
 
 
 # --------------------------------------------------------------------------
