@@ -40,10 +40,24 @@ int code_of(at::ScalarType t)
                                            : -1;
 }
 
+// Whether memory holds the tensor's values: that of a wrapper (a transform's,
+// a subclass's), a sparse matrix or a lazy negative does not.
+bool in_memory(const at::Tensor &t)
+{
+    if (!t.has_storage() || t.layout() != at::kStrided || t.is_neg()) return false;
+    try {
+        return t.numel() == 0 || t.const_data_ptr();
+    } catch (const c10::Error &) {
+        return false;
+    }
+}
+
 const at::Tensor &tensor(PyObject *o, const char *name)
 {
     TORCH_CHECK_VALUE(THPVariable_Check(o), name, " must be a tensor");
-    return THPVariable_Unpack(o);
+    const at::Tensor &t = THPVariable_Unpack(o);
+    TORCH_CHECK_VALUE(in_memory(t), name, " must be a plain dense tensor with memory of its own");
+    return t;
 }
 
 void same_device(const at::Tensor &t, const char *name, c10::Device device)
@@ -183,16 +197,29 @@ class Stream {
     bool other_ = false;
 };
 
-// A C call with `device` current; CPError for a status other than CP_OK.
-template <typename F>
-void call(const char *name, c10::Device device, F f)
+// Python's lock, given up while this lives.
+class Unlocked {
+  public:
+    Unlocked() : python_(PyEval_SaveThread()) {}
+    ~Unlocked() { PyEval_RestoreThread(python_); }
+    Unlocked(const Unlocked &) = delete;
+    Unlocked &operator=(const Unlocked &) = delete;
+
+  private:
+    PyThreadState *python_;
+};
+
+// A C call with `device` current; CPError for a status other than CP_OK. Its
+// arguments, tensors' pointers among them, are made before Python's lock is
+// given up: to make them can fail.
+template <typename F, typename... Args>
+void call(const char *name, c10::Device device, F f, Args... args)
 {
     cp_status st;
     {
         const c10::DeviceGuard guard(device);
-        PyThreadState *const python = PyEval_SaveThread();  // (a launch may wait for room in its queue)
-        st = f();
-        PyEval_RestoreThread(python);
+        const Unlocked unlocked;  // (a launch may wait for room in its queue)
+        st = f(args...);
     }
     if (st == CP_OK) return;
     PyObject *const e = PyObject_CallFunction(cp_error, "is", (int)st, name);
@@ -288,10 +315,8 @@ PyObject *embed_lookup(PyObject *, PyObject *const *arg, Py_ssize_t count)
         bad = ptr<int32_t>(b);
     }
     const float scale = (float)number(arg[2]);
-    call("cp_embed_lookup", device, [&] {
-        return cp_embed_lookup(ptr(table), (cp_dtype)code_of(table.scalar_type()), rows, d, stride, ptr<int64_t>(ids), n,
-                               scale, ptr(out), (cp_dtype)code_of(out.scalar_type()), bad, stream.handle());
-    });
+    call("cp_embed_lookup", device, cp_embed_lookup, ptr(table), (cp_dtype)code_of(table.scalar_type()), rows, d,
+         stride, ptr<int64_t>(ids), n, scale, ptr(out), (cp_dtype)code_of(out.scalar_type()), bad, stream.handle());
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }
@@ -313,10 +338,8 @@ PyObject *embed_plan(PyObject *, PyObject *const *arg, Py_ssize_t count)
     for (const at::Tensor &t : {order, slot, unique, starts, number}) stream.keep(t);
     const uint64_t need = cp_embed_plan_workspace_bytes(n, rows);
     const at::Tensor ws = stream.workspace(need, device);
-    call("cp_embed_plan", device, [&] {
-        return cp_embed_plan(ptr<int64_t>(ids), n, rows, ptr<int32_t>(order), ptr<int32_t>(slot), ptr<int64_t>(unique),
-                             ptr<int32_t>(starts), ptr<int64_t>(number), ptr(ws), need, stream.handle());
-    });
+    call("cp_embed_plan", device, cp_embed_plan, ptr<int64_t>(ids), n, rows, ptr<int32_t>(order), ptr<int32_t>(slot),
+         ptr<int64_t>(unique), ptr<int32_t>(starts), ptr<int64_t>(number), ptr(ws), need, stream.handle());
     return tuple({order, slot, unique, starts, number});
     END_HANDLE_TH_ERRORS
 }
@@ -348,12 +371,9 @@ PyObject *embed_grad(PyObject *, PyObject *const *arg, Py_ssize_t count)
     stream.keep(grad);
     const uint64_t need = cp_embed_grad_workspace_bytes(n, d);
     const at::Tensor ws = stream.workspace(need, device);
-    call("cp_embed_grad", device, [&] {
-        return cp_embed_grad(ptr<int32_t>(order), ptr<int32_t>(slot), ptr<int64_t>(unique), ptr<int32_t>(starts),
-                             ptr<int64_t>(number_of), n, all ? table_rows : 0, ptr(dout),
-                             (cp_dtype)code_of(dout.scalar_type()), d, stride, scale, ptr<float>(grad), ptr(ws), need,
-                             stream.handle());
-    });
+    call("cp_embed_grad", device, cp_embed_grad, ptr<int32_t>(order), ptr<int32_t>(slot), ptr<int64_t>(unique),
+         ptr<int32_t>(starts), ptr<int64_t>(number_of), n, all ? table_rows : 0, ptr(dout),
+         (cp_dtype)code_of(dout.scalar_type()), d, stride, scale, ptr<float>(grad), ptr(ws), need, stream.handle());
     return wrapped(grad);
     END_HANDLE_TH_ERRORS
 }
@@ -389,11 +409,9 @@ PyObject *rms_norm(PyObject *, PyObject *const *arg, Py_ssize_t count)
     if (truth(arg[6])) rstd = empty({n}, at::ScalarType::Float, device);
     for (const at::Tensor &t : {y, q, scale, rstd}) stream.keep(t);
     if (n)
-        call("cp_rms_norm", device, [&] {
-            return cp_rms_norm(ptr(x), stride, ptr(residual), residual_stride, ptr(weight), (cp_dtype)code_of(type), n, d,
-                               eps, ptr(h), ptr(y), ptr<uint8_t>(q), eight ? q.stride(0) : 0, ptr<uint8_t>(scale),
-                               eight ? scale.stride(0) : 0, ptr<float>(rstd), stream.handle());
-        });
+        call("cp_rms_norm", device, cp_rms_norm, ptr(x), stride, ptr(residual), residual_stride, ptr(weight),
+             (cp_dtype)code_of(type), n, d, eps, ptr(h), ptr(y), ptr<uint8_t>(q), eight ? q.stride(0) : 0,
+             ptr<uint8_t>(scale), eight ? scale.stride(0) : 0, ptr<float>(rstd), stream.handle());
     return tuple({residual.defined() ? h : x, y, q, scale, rstd});
     END_HANDLE_TH_ERRORS
 }
@@ -424,10 +442,9 @@ PyObject *rms_norm_grad(PyObject *, PyObject *const *arg, Py_ssize_t count)
     stream.keep(dw);
     const uint64_t need = cp_rms_norm_grad_workspace_bytes(n, d);
     const at::Tensor ws = stream.workspace(need, device);
-    call("cp_rms_norm_grad", device, [&] {
-        return cp_rms_norm_grad(ptr(dy), dy_stride, ptr(x), stride, ptr<float>(rstd), ptr(weight), ptr(dres), dres_stride,
-                                (cp_dtype)code_of(type), n, d, ptr(dx), ptr<float>(dw), ptr(ws), need, stream.handle());
-    });
+    call("cp_rms_norm_grad", device, cp_rms_norm_grad, ptr(dy), dy_stride, ptr(x), stride, ptr<float>(rstd),
+         ptr(weight), ptr(dres), dres_stride, (cp_dtype)code_of(type), n, d, ptr(dx), ptr<float>(dw), ptr(ws), need,
+         stream.handle());
     return tuple({dx, dw});
     END_HANDLE_TH_ERRORS
 }
@@ -452,12 +469,9 @@ PyObject *quantize_fp8(PyObject *, PyObject *const *arg, Py_ssize_t count)
     }
     for (const at::Tensor &t : {q, scale, qt, scale_t}) stream.keep(t);
     if (n && d)
-        call("cp_quantize_fp8", device, [&] {
-            return cp_quantize_fp8(ptr(x), (cp_dtype)code_of(x.scalar_type()), n, d, stride, blocks, ptr<uint8_t>(q),
-                                   q.stride(0), ptr<uint8_t>(scale), scale.stride(0), ptr<uint8_t>(qt),
-                                   both ? qt.stride(0) : 0, ptr<uint8_t>(scale_t), both ? scale_t.stride(0) : 0,
-                                   stream.handle());
-        });
+        call("cp_quantize_fp8", device, cp_quantize_fp8, ptr(x), (cp_dtype)code_of(x.scalar_type()), n, d, stride,
+             blocks, ptr<uint8_t>(q), q.stride(0), ptr<uint8_t>(scale), scale.stride(0), ptr<uint8_t>(qt),
+             both ? qt.stride(0) : 0, ptr<uint8_t>(scale_t), both ? scale_t.stride(0) : 0, stream.handle());
     return tuple({q, scale, qt, scale_t});
     END_HANDLE_TH_ERRORS
 }
@@ -515,11 +529,9 @@ PyObject *gemm_fp8(PyObject *, PyObject *const *arg, Py_ssize_t count)
     }
     const uint64_t need = cp_gemm_fp8_workspace_bytes(m, n, k, (cp_dtype)code_of(type));
     const at::Tensor ws = stream.workspace(need, device);
-    call("cp_gemm_fp8", device, [&] {
-        return cp_gemm_fp8(ptr<uint8_t>(a), a_stride, ptr<uint8_t>(a_scale), as_stride, ptr<uint8_t>(b), b_stride,
-                           ptr<uint8_t>(b_scale), bs_stride, !by_row, m, n, k, ptr(out), out_stride,
-                           (cp_dtype)code_of(type), ptr(ws), need, stream.handle());
-    });
+    call("cp_gemm_fp8", device, cp_gemm_fp8, ptr<uint8_t>(a), a_stride, ptr<uint8_t>(a_scale), as_stride,
+         ptr<uint8_t>(b), b_stride, ptr<uint8_t>(b_scale), bs_stride, !by_row, m, n, k, ptr(out), out_stride,
+         (cp_dtype)code_of(type), ptr(ws), need, stream.handle());
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }
