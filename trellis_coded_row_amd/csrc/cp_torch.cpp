@@ -14,6 +14,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -57,6 +58,10 @@ const at::Tensor &tensor(PyObject *o, const char *name)
     TORCH_CHECK_VALUE(THPVariable_Check(o), name, " must be a tensor");
     const at::Tensor &t = THPVariable_Unpack(o);
     TORCH_CHECK_VALUE(in_memory(t), name, " must be a plain dense tensor with memory of its own");
+    // a result without its gradient's graph would end the caller's backward pass there, silently
+    TORCH_CHECK_VALUE(!t.requires_grad() || !c10::GradMode::is_enabled(), name,
+                      " requires a gradient, which this function does not record: pass a detached tensor, or call it "
+                      "under torch.no_grad() (a gradient's function is a call of its own)");
     return t;
 }
 

@@ -20,6 +20,11 @@ its handle) does not wait for the current one: its inputs have to be ready
 there and stay alive until it is done. What it allocates comes from that
 stream's memory; an output may be dropped on the current stream after use there.
 
+Nothing is recorded for autograd: the gradients are functions of their own, to
+be called from a backward pass (an autograd function's forward and backward run
+without recording). A tensor that requires a gradient is refused while torch
+records, as its gradient would be lost.
+
 8-bit matrices are ``torch.float8_e4m3fn`` with ``torch.float8_e8m0fnu``
 scales. Those made here have rows that start on 16 bytes (4 for scales), as
 ``gemm_fp8`` needs them; a matrix and its scales share one allocation.
