@@ -134,6 +134,12 @@ EightBits empty_eight_bits(int64_t rows, int64_t cols, int64_t srows, int64_t sc
     return t;
 }
 
+// A caller's tensor was written: autograd then refuses to use it as a value saved before.
+void written(const at::Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void *ptr(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 template <typename T>
@@ -322,6 +328,8 @@ PyObject *embed_lookup(PyObject *, PyObject *const *arg, Py_ssize_t count)
     const float scale = (float)number(arg[2]);
     call("cp_embed_lookup", device, cp_embed_lookup, ptr(table), (cp_dtype)code_of(table.scalar_type()), rows, d,
          stride, ptr<int64_t>(ids), n, scale, ptr(out), (cp_dtype)code_of(out.scalar_type()), bad, stream.handle());
+    if (arg[4] != Py_None) written(out);
+    if (bad) written(tensor(arg[5], "bad_id"));
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }
@@ -537,6 +545,7 @@ PyObject *gemm_fp8(PyObject *, PyObject *const *arg, Py_ssize_t count)
     call("cp_gemm_fp8", device, cp_gemm_fp8, ptr<uint8_t>(a), a_stride, ptr<uint8_t>(a_scale), as_stride,
          ptr<uint8_t>(b), b_stride, ptr<uint8_t>(b_scale), bs_stride, !by_row, m, n, k, ptr(out), out_stride,
          (cp_dtype)code_of(type), ptr(ws), need, stream.handle());
+    if (arg[5] != Py_None) written(out);
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }
