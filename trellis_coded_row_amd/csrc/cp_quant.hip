@@ -203,22 +203,28 @@ __global__ __launch_bounds__(kThreads) void quantize_tile(const typename Elem<DT
     }
 }
 
+// Tiles of one launch, at most: its threads are counted in 32 bits, and a
+// launch of more than 2^32 runs the remainder alone, without an error.
+constexpr uint64_t kLaunchTiles = 1ull << 22;
+static_assert(kLaunchTiles * kThreads < (1ull << 32), "");
+
 template <int DT, bool BLOCKS, bool TRANS>
 hipError_t launch(const QuantArgs &a)
 {
-    const uint64_t tiles_x = div_up(a.d, kTile);
-    // whole rows of tiles per launch, fewer than 2^32 threads in each
-    uint64_t step = (1ull << 22) / tiles_x;
-    if (step == 0) step = 1;
-    const uint64_t tiles_y = div_up(a.n, kTile);
-    for (uint64_t y = 0; y < tiles_y; y += step) {
-        const uint64_t r = y * kTile, ny = tiles_y - y < step ? tiles_y - y : step;
+    const uint64_t tiles_x = div_up(a.d, kTile), tiles_y = div_up(a.n, kTile);
+    const uint64_t step_x = tiles_x < kLaunchTiles ? tiles_x : kLaunchTiles, step_y = kLaunchTiles / step_x;
+    for (uint64_t y = 0; y < tiles_y; y += step_y) {
+        const uint64_t r = y * kTile, ny = tiles_y - y < step_y ? tiles_y - y : step_y;
         const uint64_t n = a.n - r < ny * kTile ? a.n - r : ny * kTile;
-        quantize_tile<DT, BLOCKS, TRANS><<<(uint32_t)(ny * tiles_x), kThreads, 0, a.stream>>>(
-            (const typename Elem<DT>::raw *)a.x + r * a.x_stride, (uint32_t)n, (uint32_t)a.d, a.x_stride,
-            (uint32_t)tiles_x, a.q + r * a.q_stride, a.q_stride, a.scale + (BLOCKS ? y : r) * a.scale_stride,
-            a.scale_stride, TRANS ? a.qt + r : nullptr, a.qt_stride, TRANS ? a.scale_t + y : nullptr,
-            a.scale_t_stride);
+        for (uint64_t x = 0; x < tiles_x; x += step_x) {
+            const uint64_t c = x * kTile, nx = tiles_x - x < step_x ? tiles_x - x : step_x;
+            const uint64_t d = a.d - c < nx * kTile ? a.d - c : nx * kTile;
+            quantize_tile<DT, BLOCKS, TRANS><<<(uint32_t)(ny * nx), kThreads, 0, a.stream>>>(
+                (const typename Elem<DT>::raw *)a.x + r * a.x_stride + c, (uint32_t)n, (uint32_t)d, a.x_stride,
+                (uint32_t)nx, a.q + r * a.q_stride + c, a.q_stride, a.scale + (BLOCKS ? y : r) * a.scale_stride + x,
+                a.scale_stride, TRANS ? a.qt + c * a.qt_stride + r : nullptr, a.qt_stride,
+                TRANS ? a.scale_t + (BLOCKS ? x : c) * a.scale_t_stride + y : nullptr, a.scale_t_stride);
+        }
     }
     return hipGetLastError();
 }
