@@ -13,7 +13,10 @@ namespace cpk {
 
 namespace {
 
-constexpr uint64_t kMaxRows = 1u << 21;  // rows of one launch, at most
+// Rows or workgroups of one launch, at most: its threads (1,024 a workgroup)
+// are counted in 32 bits, and a launch of more than 2^32 runs the remainder
+// alone, without an error.
+constexpr uint64_t kMaxRows = 1u << 21;
 
 // Sum over the W waves that share a row (W == 1: the wave alone).
 template <int W>
@@ -331,16 +334,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_grad_rows(
     }
 }
 
-// Rows too long for registers: dx alone, the row read twice.
+// Rows too long for registers, from row `first` on: dx alone, the row read twice.
 template <int DT>
 __global__ __launch_bounds__(kLongWaves * 64) void norm_grad_long(
     const typename Elem<DT>::raw *__restrict__ dy, uint64_t dy_stride, const typename Elem<DT>::raw *__restrict__ x,
     uint64_t x_stride, const float *__restrict__ rstd, const typename Elem<DT>::raw *__restrict__ weight,
-    const typename Elem<DT>::raw *__restrict__ dres, uint64_t dres_stride, uint32_t d,
+    const typename Elem<DT>::raw *__restrict__ dres, uint64_t dres_stride, uint64_t first, uint32_t d,
     typename Elem<DT>::raw *__restrict__ dx)
 {
     __shared__ float part[kLongWaves];
-    const uint64_t row = blockIdx.x;
+    const uint64_t row = first + blockIdx.x;
     const float rs = rstd[row];
     float mean = 0.0f;
     for (int pass = 0; pass < 2; ++pass) {
@@ -390,14 +393,14 @@ __global__ __launch_bounds__(256) void norm_grad_long_dw(const typename Elem<DT>
     store8<kF32>(partial + (uint64_t)blockIdx.y * d, c, d, dw);
 }
 
-// dw = the sum of the partial rows: 32 columns per workgroup, 32 threads a
-// column, joined in a fixed order.
-__global__ __launch_bounds__(1024) void sum_partials(const float *__restrict__ partial, uint32_t count, uint32_t d,
-                                                     float *__restrict__ dw)
+// dw = the sum of the partial rows: 32 columns per workgroup (workgroup 0 has
+// those from 32 first on), 32 threads a column, joined in a fixed order.
+__global__ __launch_bounds__(1024) void sum_partials(const float *__restrict__ partial, uint32_t count,
+                                                     uint32_t first, uint32_t d, float *__restrict__ dw)
 {
     __shared__ float sums[32][33];
     const uint32_t lane = threadIdx.x & 31u, g = threadIdx.x >> 5;
-    const uint32_t c = blockIdx.x * 32u + lane;
+    const uint32_t c = (first + blockIdx.x) * 32u + lane;
     float s = 0.0f;
     if (c < d) {
 #pragma unroll 8
@@ -455,17 +458,21 @@ hipError_t grad_of(const NormGradArgs &a)
     else if (a.d <= 24576) grad_launch<DT, 16, 3>(a);
     else if (a.d <= kGradRegColumns) grad_launch<DT, 16, 4>(a);
     else {
-        norm_grad_long<DT><<<(uint32_t)a.n, kLongWaves * 64, 0, a.stream>>>(
-            (const R *)a.dy, a.dy_stride, (const R *)a.x, a.x_stride, a.rstd, (const R *)a.weight, (const R *)a.dres,
-            a.dres_stride, (uint32_t)a.d, (R *)a.dx);
+        for (uint64_t row = 0; row < a.n; row += kMaxRows)
+            norm_grad_long<DT><<<(uint32_t)(a.n - row < kMaxRows ? a.n - row : kMaxRows), kLongWaves * 64, 0, a.stream>>>(
+                (const R *)a.dy, a.dy_stride, (const R *)a.x, a.x_stride, a.rstd, (const R *)a.weight, (const R *)a.dres,
+                a.dres_stride, row, (uint32_t)a.d, (R *)a.dx);
         if (a.dw)
             norm_grad_long_dw<DT><<<dim3((uint32_t)div_up(a.d, 2048), grad_partials(a.n, a.d)), 256, 0, a.stream>>>(
                 (const R *)a.dy, a.dy_stride, (const R *)a.x, a.x_stride, a.rstd, (uint32_t)a.n, (uint32_t)a.d,
                 (float *)a.workspace);
     }
-    if (a.dw)
-        sum_partials<<<(uint32_t)div_up(a.d, 32), 1024, 0, a.stream>>>((const float *)a.workspace,
-                                                                       grad_partials(a.n, a.d), (uint32_t)a.d, a.dw);
+    if (a.dw) {
+        const uint64_t blocks = div_up(a.d, 32);
+        for (uint64_t b = 0; b < blocks; b += kMaxRows)
+            sum_partials<<<(uint32_t)(blocks - b < kMaxRows ? blocks - b : kMaxRows), 1024, 0, a.stream>>>(
+                (const float *)a.workspace, grad_partials(a.n, a.d), (uint32_t)b, (uint32_t)a.d, a.dw);
+    }
     return hipGetLastError();
 }
 
@@ -475,7 +482,7 @@ hipError_t rms_norm(const NormArgs &args)
 {
     NormArgs a = args;
     const uint64_t es = dtype_bytes(a.dtype);
-    for (uint64_t left = args.n; left > 0;) {  // a launch has fewer than 2^32 threads
+    for (uint64_t left = args.n; left > 0;) {
         a.n = left < kMaxRows ? left : kMaxRows;
         const hipError_t e = a.dtype == kF32    ? norm_type<kF32>(a)
                              : a.dtype == kBF16 ? norm_type<kBF16>(a)
