@@ -497,7 +497,7 @@ int64_t operand(const at::Tensor &t, const char *name, at::ScalarType type, int6
     int64_t stride = rows_of(t, name);
     same_device(t, name, device);
     const int64_t rows = t.size(0), cols = t.size(1), wide = up(cols, unit);
-    if (rows <= 1) stride = wide;
+    if (rows <= 1 || cols == 0) stride = wide;  // nothing goes by it
     if (rows && cols) {
         TORCH_CHECK_VALUE(stride % unit == 0 && stride >= wide && (uintptr_t)t.data_ptr() % unit == 0, "the rows of ",
                           name, " must start on ", unit, " bytes");
