@@ -175,8 +175,8 @@ uint64_t cp_gemm_fp8_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, cp_dtyp
  * full, from each operand's scaled values, which have to lie within the
  * range of 32-bit floating point (those below 2^-124 may lose bits).
  * workspace - device, 256-byte aligned.
- * Errors: INVALID_ARGUMENT, UNSUPPORTED (a stride above 2^22, or m or n above
- * 2^25), HIP. */
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (a stride above 2^22, m or n above
+ * 2^25, or an output of 2^24 tiles of 256 x 128 or more), HIP. */
 cp_status cp_gemm_fp8(const uint8_t *a, uint64_t a_stride, const uint8_t *a_scale, uint64_t a_scale_stride,
                       const uint8_t *b, uint64_t b_stride, const uint8_t *b_scale, uint64_t b_scale_stride,
                       int b_blocks, uint64_t m, uint64_t n, uint64_t k, void *out, uint64_t out_stride,

@@ -8,7 +8,8 @@ static constexpr uint64_t kMaxCount = 0x7FFFFFFFull;           // lengths that k
 static constexpr uint64_t kMaxSorted = 0x7FFFFFFFull - 4095;   // ids of one plan
 static constexpr uint64_t kMaxGradColumns = 1ull << 21;        // a launch has fewer than 2^16 workgroups along y
 static constexpr uint64_t kMaxGemmStride = 1ull << 22;         // a tile's rows then lie within 2^31 bytes
-static constexpr uint64_t kMaxGemmRows = 1ull << 25;         // launches then have fewer than 2^32 threads
+static constexpr uint64_t kMaxGemmRows = 1ull << 25;           // a launch for few rows of A then has fewer than 2^32 threads
+static constexpr uint64_t kMaxGemmTiles = 1ull << 24;          // as one of tiles, of 256 threads each, then has
 
 static bool dtype_ok(cp_dtype t) { return t == CP_DTYPE_F32 || t == CP_DTYPE_BF16 || t == CP_DTYPE_F16; }
 
@@ -21,6 +22,12 @@ static bool good_or_null(const void *p, uint64_t bytes) { return ((uintptr_t)p &
 static bool spans(uint64_t n, uint64_t stride, uint64_t bytes)
 {
     return n == 0 || stride <= (1ull << 62) / bytes / n;
+}
+
+// A product whose largest tiles (256 x 128, or twice that) are too many for a launch.
+static bool too_many_tiles(uint64_t m, uint64_t n)
+{
+    return cpk::div_up(m, 256) * cpk::div_up(n, 128) >= kMaxGemmTiles;
 }
 
 static bool workspace_ok(const void *p, uint64_t bytes, uint64_t need)
@@ -254,7 +261,9 @@ cp_status cp_quantize_fp8(const void *x, cp_dtype dtype, uint64_t n, uint64_t d,
 
 uint64_t cp_gemm_fp8_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, cp_dtype out_dtype)
 {
-    if (!dtype_ok(out_dtype) || m == 0 || n == 0 || k == 0 || m > kMaxGemmRows || n > kMaxGemmRows || k > kMaxGemmStride) return 0;
+    if (!dtype_ok(out_dtype) || m == 0 || n == 0 || k == 0 || m > kMaxGemmRows || n > kMaxGemmRows ||
+        k > kMaxGemmStride || too_many_tiles(m, n))
+        return 0;
     return cpk::gemm_fp8_workspace_bytes(m, n, k, out_dtype);
 }
 
@@ -269,7 +278,7 @@ cp_status cp_gemm_fp8(const uint8_t *a, uint64_t a_stride, const uint8_t *a_scal
         b_scale_stride < groups || a_scale_stride % 4 || b_scale_stride % 4 || out_stride < n)
         return CP_ERR_INVALID_ARGUMENT;
     if (m > kMaxGemmRows || n > kMaxGemmRows || a_stride > kMaxGemmStride || b_stride > kMaxGemmStride ||
-        a_scale_stride > kMaxGemmStride || b_scale_stride > kMaxGemmStride)
+        a_scale_stride > kMaxGemmStride || b_scale_stride > kMaxGemmStride || too_many_tiles(m, n))
         return CP_ERR_UNSUPPORTED;
     if (!spans(m, out_stride, 4)) return CP_ERR_INVALID_ARGUMENT;
     if (m == 0 || n == 0) return CP_OK;
