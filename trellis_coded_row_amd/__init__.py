@@ -592,9 +592,7 @@ class MixedTable(Table):
         return out
 
 
-# the dense operators: ops.py builds on the names above, and on a library of its own
-if not os.path.exists(_build.TORCH_LIB):
-    _build.build_torch()
+# the dense operators: ops.py builds on the names above
 from . import ops as _ops  # noqa: E402
 from .ops import *  # noqa: E402,F401,F403
 

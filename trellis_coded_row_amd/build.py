@@ -4,8 +4,10 @@ probes, include/cp_probe.h) and _cp_torch.so (the dense operators' functions on
 torch tensors, host code on top of libcp.so)."""
 from __future__ import annotations
 
+import hashlib
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -28,6 +30,7 @@ PROBE_SOURCES = [os.path.join(CSRC, "cp_probe.hip")]
 PROBE_LIB = os.path.join(PKG, "libcp_probe.so")
 TORCH_SOURCE = os.path.join(CSRC, "cp_torch.cpp")
 TORCH_LIB = os.path.join(PKG, "_cp_torch.so")
+TORCH_DEPS = [TORCH_SOURCE, os.path.join(ROOT, "include", "cp.h"), os.path.join(ROOT, "include", "cp_ops.h")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -77,16 +80,48 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     return lib
 
 
+def _torch_folder() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]  # without importing it
+
+
+def _torch_mark() -> str:
+    """What _cp_torch.so carries of the torch it was built for."""
+    with open(os.path.join(_torch_folder(), "version.py")) as f:
+        version = re.search(r"__version__ = '([^']*)'", f.read()).group(1)
+    return f"[built for torch {version}]"
+
+
+def _source_mark() -> str:
+    """What it carries of its sources."""
+    digest = hashlib.sha256()
+    for path in TORCH_DEPS:
+        with open(path, "rb") as f:
+            digest.update(f.read())
+    return f"[built from {digest.hexdigest()[:16]}]"
+
+
+def torch_built() -> tuple[bool, bool]:
+    """Whether _cp_torch.so is there, built for the torch that is installed,
+    and whether it is built from the present sources (where there are any)."""
+    if not os.path.exists(TORCH_LIB):
+        return False, False
+    with open(TORCH_LIB, "rb") as f:
+        held = f.read()
+    sources = all(os.path.exists(p) for p in TORCH_DEPS)
+    return _torch_mark().encode() in held, not sources or _source_mark().encode() in held
+
+
 def build_torch(verbose: bool = False) -> str:
     """Builds _cp_torch.so, a CPython module, against the torch that is
     installed and libcp.so beside it."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]  # its folder, without importing it
+    torch = _torch_folder()
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc()))) if os.path.isabs(hipcc()) else "/opt/rocm"
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
     tmp = TORCH_LIB + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D__HIP_PLATFORM_AMD__=1",  # what hipcc itself defines; the HIP headers ask for it
+           '-DCP_TORCH_MARKS="%s"' % " ".join((_torch_mark(), _source_mark())),
            *(x for d in include for x in ("-isystem", d)), TORCH_SOURCE, "-o", tmp,
            "-L", PKG, "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"),
            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]

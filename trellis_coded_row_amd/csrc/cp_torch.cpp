@@ -27,6 +27,9 @@ namespace {
 constexpr int64_t kGroup = 128;  // values that share a scale
 constexpr auto kE4m3 = at::ScalarType::Float8_e4m3fn, kE8m0 = at::ScalarType::Float8_e8m0fnu;
 
+// What this was built for and from, as build.py looks for it in the file.
+[[gnu::used]] const char marks[] = CP_TORCH_MARKS;
+
 PyObject *cp_error = nullptr;  // CPError(status, name)
 
 int64_t up(int64_t v, int64_t unit) { return (v + unit - 1) / unit * unit; }

@@ -13,7 +13,8 @@ returned); the others take torch tensors on one GPU, allocate their outputs,
 and raise ``ValueError`` for tensors they do not take and ``CPError`` for a
 status other than CP_OK. Their checks, outputs and workspaces are made in C++
 (``csrc/cp_torch.cpp``), as the calls of a single token's step take no longer
-than their host side.
+than their host side; where that library can be neither loaded nor built (no
+compiler, for one), they raise ``ImportError`` and the rest of the package works.
 
 ``stream=None`` is torch's current stream. A call on another one (a stream or
 its handle) does not wait for the current one: its inputs have to be ready
@@ -32,12 +33,13 @@ scales. Those made here have rows that start on 16 bytes (4 for scales), as
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import CPError, _L, library_path
-from . import _cp_torch as _torch
+from . import build as _build
 
 __all__ = [
     "CP_DTYPE_F32", "CP_DTYPE_BF16", "CP_DTYPE_F16", "FP8_GROUP",
@@ -82,7 +84,36 @@ cp_gemm_fp8 = _bind("cp_gemm_fp8", _int, _vp, _u64, _vp, _u64, _vp, _u64, _vp, _
                     _int, _vp, _u64, _vp)
 
 
-_torch.setup(CPError)
+class _Unavailable:
+    """In place of the C++ functions where they can be neither loaded nor
+    built: the coded table does without them, a dense operator raises."""
+
+    def __init__(self, reason: Exception):
+        self.reason = reason
+
+    def __getattr__(self, name):
+        raise ImportError(f"{_build.TORCH_LIB}, which {name} runs on, can be neither loaded nor built: "
+                          f"{type(self.reason).__name__}: {self.reason}") from self.reason
+
+
+def _load_torch():
+    """The functions of csrc/cp_torch.cpp; built first if they are not, or for
+    another torch than the present one."""
+    try:
+        usable, present = _build.torch_built()
+        if not usable:
+            _build.build_torch()
+        elif not present:
+            warnings.warn(f"{_build.TORCH_LIB} is older than its sources; rebuild it "
+                          "(python trellis_coded_row_amd/build.py)", stacklevel=2)
+        from . import _cp_torch
+        _cp_torch.setup(CPError)
+    except Exception as e:
+        return _Unavailable(e)
+    return _cp_torch
+
+
+_torch = _load_torch()
 
 
 # --------------------------------------------------------------------------
