@@ -207,5 +207,7 @@ def gemm_fp8(a, a_scale, b, b_scale, dtype=torch.bfloat16, out=None, stream=None
     """out [m, n] = A B^T of e4m3 matrices a [m, k] and b [n, k] with e8m0
     scales: a_scale [m, ceil(k / 128)], and b_scale either [n, ceil(k / 128)]
     or, one for each 128 x 128 block, [ceil(n / 128), ceil(k / 128)].
-    Products are summed in 32 bits; dtype is float32, bfloat16 or float16."""
+    dtype is float32, bfloat16 or float16. Sums run in 32 bits; for the 16-bit
+    types, of each 8 neighbouring products those far below the largest lose
+    what lies 2^-13 below it (include/cp_ops.h), for float32 none does."""
     return _torch.gemm_fp8(a, a_scale, b, b_scale, dtype, out, stream)
