@@ -126,8 +126,9 @@ cp_status cp_rms_norm(const void *x, uint64_t x_stride, const void *residual, ui
 /* Device workspace bytes of cp_rms_norm_grad. */
 uint64_t cp_rms_norm_grad_workspace_bytes(uint64_t n, uint64_t d);
 
-/* The norm's gradient. x is the norm's input (h, where there was a residual)
- * and rstd what the forward pass stored:
+/* The norm's gradient. x is the norm's input (h_out, where there was a
+ * residual: rounded, while the forward pass took y and rstd from the unrounded
+ * h) and rstd what the forward pass stored:
  *   xhat = x * rstd, g = dy * weight,
  *   dx = rstd * (g - xhat * mean(g * xhat)) + dres (dres may be NULL),
  *   dw[c] = sum over rows of dy * xhat, in 32 bits (float[d]).

@@ -22,10 +22,14 @@
 // rms, the 32-bit sum's own rounding), at half the rate and with the
 // conversions beside it.
 //
-// Reached: 4,096 x 4,096 x 24,576 to bf16 in 308 us, 2.68 PFLOP/s (the vendor
-// library's product with one scale for each operand: 303 us); 4,096 x 24,576 x
-// 4,096 to 32 bits in 800 us, 1.03 PFLOP/s (its bf16 product, with a 16-bit
-// output: 652 us); 8 x 4,096 x 24,576 in 22.6 us, 4.5 TB/s (a copy: 5.0).
+// Reached: 4,096 x 4,096 x 24,576 to bf16 in 300 us, 2.75 PFLOP/s, where the
+// vendor library's product of the same operands with one scale for each takes
+// 250 in turn with it; 4,096 x 24,576 x 4,096 to 32 bits in 790 us, 1.04 PFLOP/s
+// (its product of operands widened before, with a 16-bit output: 490); 8 x 4,096 x
+// 24,576 in 22.6 us, 4.5 TB/s (a copy: 5.0 to 5.2). A run of long products lowers
+// the clock for some milliseconds after a pause: 300 is 320 to 450 there, 790 up
+// to 1,100. These sizes fill the chip with whole rounds of the largest tile;
+// others are 1.5 to 5 times as far from the library's rate (see cut_of).
 //
 // The operands are passed swapped (B's rows as the instruction's rows), so
 // that a lane's four results are neighbours in an output row.
@@ -814,7 +818,10 @@ __global__ __launch_bounds__(256) void join_splits(const float *__restrict__ par
     }
 }
 
-// Few rows of A (16 MT at most): B is read once and bounds the time. A
+// Few rows of A (16 MT at most): B is read once and, up to 16 rows, bounds the
+// time. 32 rows of the product above take 39 us and 64 take 62: each of its 256
+// workgroups reads all of A from L2, 0.2 and 0.4 GB together (and five of the
+// eight forms of 64 rows spill 4 to 15 registers). A
 // workgroup has 16 columns of the output; its W waves take runs of steps of
 // k, straight into registers, and add their sums through LDS. A wave reads
 // the next U steps while it multiplies U: 8 KiB of B in flight for each of
@@ -958,7 +965,15 @@ Cut cut_of(uint64_t m, uint64_t n, uint64_t k, bool exact)
     }
     // time of each cut in cycles of one compute unit: rounds of workgroups
     // times their steps, the work of a step by tile size, a start and an end
-    // per workgroup, and the pass that joins splits
+    // per workgroup, and the pass that joins splits. (per_cu is what LDS allows
+    // and the other figures were fitted with. The registers allow less in some
+    // forms: one workgroup of the 128 x 128 tile with a 32-bit output or an end
+    // of k inside a step, three of the 64 x 64 one with a 32-bit output. In a
+    // sweep of 40 sizes the rule's cut took 3% more than the best of all on
+    // average and 29% at most. With a 16-bit output, 128 x 128 tiles take
+    // in a step's copies in twice the time of its products, so sizes that do
+    // not fill the chip with 256 x 256 tiles run at half the rate or less:
+    // 939 x 1,664 x 4,992 takes 25 us where the operations alone are 5.)
     double least = 0;
     struct Kind { int fm, fn; double step, ends; uint32_t per_cu; };
     static const Kind narrow[] = {{8, 8, 2430, 6000, 1}, {4, 4, 900, 4000, 2}, {2, 2, 330, 3000, 4}};

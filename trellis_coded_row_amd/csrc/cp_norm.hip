@@ -5,8 +5,13 @@
 //   dx = rstd (g - xhat mean(g xhat)) + dres, g = dy w, xhat = x rstd
 //   dw = sum over rows of dy xhat
 //
-// Both are bound by memory: a row is read once and stays in registers
-// between its reduction and its outputs. Sums run in 32 bits.
+// Both are bound by memory: a row of up to 32,768 columns is read once and
+// stays in registers between its reduction and its outputs (in the gradient of
+// more than 16,384 columns some of it in scratch memory, see there); longer
+// ones are read twice. Sums run in 32 bits.
+//
+// h stays in 32 bits on its way to y and rstd. The gradient is taken at the h
+// that was stored, which is rounded: in 16 bits, at slightly another point.
 #include "cp_ops_internal.h"
 
 namespace cpk {
@@ -83,7 +88,10 @@ constexpr uint32_t kAheadWaves = 4096;  // waves that stay: four for each SIMD u
 //
 // Bound by memory: 4,096 bf16 rows of 24,576 to 8 bits take 63 us, 4.8 TB/s (a
 // copy reaches 5.0). With one row per workgroup, none read ahead, 73 us: then
-// a workgroup's loads, its barrier and its stores follow one another.
+// a workgroup's loads, its barrier and its stores follow one another. That is
+// how rows too long to be read ahead go (kAhead): the same rows with a residual
+// take 132 us, in 32 bits 243, both 5.4 TB/s with part of them in the last level
+// cache.
 template <int DT, int W, int IT, bool RES>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_rows(
     const typename Elem<DT>::raw *__restrict__ x, uint64_t x_stride, const typename Elem<DT>::raw *__restrict__ res,
@@ -154,9 +162,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64, 4) void norm_rows(
             if (!AHEAD && (y_out || q)) vw[i] = load8<DT>(weight, c, d);
             if (!y_out && !q) continue;
             // (past the row's end, h and the weight are zero. Of 100 million
-            // 8-bit values some 50 lie so near a border that they fall on its
-            // other side than in 64 bits: as many with the product rounded
-            // once from a root in 64 bits, at 3 us more for them)
+            // 8-bit values 45 to 65 lie so near a border that they fall on its
+            // other side than in 64 bits. With a corrected root and one
+            // rounding of the product they are 40 to 60, at 2 to 3 us more:
+            // not kept; two products in 32 bits are what the formula says)
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = value(i, e) * rstd * Elem<DT>::get(vw[i][e]);
@@ -267,6 +276,13 @@ constexpr uint32_t kGradBlocks = 512;  // workgroups, each with its own rows and
 // Group g of W waves takes rows g, g + groups, ...; dw's sum over them goes
 // to partial row g. Bound by memory: 8,192 bf16 rows of 4,096 with a residual
 // take 50 us here and 5 for the sum of the partial rows, 4.9 TB/s (a copy: 5.0).
+//
+// Not so at two ends. 16 waves a row have 128 registers a lane, of which dw's
+// sums take 8 IT: up to 24,576 columns 8 of them spill in bf16 and 214 in 32
+// bits, up to 32,768 there are 173, 379 and, in fp16, 78. 4,096 rows of 24,576
+// take 173 us in bf16 and 365 in 32 bits (3.5 and 3.3 TB/s), 2,048 of 32,768
+// 379 and 406 (1.1 and 2.0 TB/s). And up to 512 rows have a partial row each,
+// written and read again: 512 x 4,096 in bf16 take 11 us, 682 x 24,576 46.
 template <int DT, int W, int IT>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_grad_rows(
     const typename Elem<DT>::raw *__restrict__ dy, uint64_t dy_stride, const typename Elem<DT>::raw *__restrict__ x,

@@ -6,10 +6,11 @@
 //
 // Bound by memory: the matrix is read once, in tiles of 128 x 128 that hold
 // whole groups of both directions, and both outputs are written from it.
-// 4,096 x 24,576 bf16 in blocks, both ways: 87 us, 4.6 TB/s (a copy: 5.0). 1,000 x
-// 2,050 (136 tiles, fewer than compute units) is a tile's latency: 6.6 us, where
-// 256 threads a tile took 8.3 (a wave alone on its SIMD unit issues slowly) and
-// testing each value for what is not finite, not the maxima, 9.8.
+// 4,096 x 24,576 bf16 in blocks, both ways: 81 to 87 us, 4.6 to 4.9 TB/s (a copy:
+// 5.0 to 5.2). 1,000 x 2,050 (136 tiles, fewer than compute units) is a tile's
+// latency: 6.7 us, where 256 threads a tile took 8.3 (a wave alone on its SIMD
+// unit issues slowly) and testing each value for what is not finite, not the
+// maxima, 9.8.
 #include <type_traits>
 
 #include "cp_ops_internal.h"
