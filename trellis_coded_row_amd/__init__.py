@@ -247,17 +247,16 @@ def shard_plan(ids, rows_per_shard: int, shards: int, stream=None):
     if not (ids.is_cuda and ids.dtype == torch.int64 and ids.dim() == 1 and ids.is_contiguous()):
         raise ValueError("ids must be a contiguous 1-D int64 device tensor")
     n = ids.shape[0]
-    local_ids = torch.empty(max(n, 1), dtype=torch.int64, device=ids.device)
-    positions = torch.empty(max(n, 1), dtype=torch.int64, device=ids.device)
-    counts = torch.empty(max(shards, 1), dtype=torch.int64, device=ids.device)
+    def made(count, dtype=torch.int64):
+        return _made_for(stream, torch.empty, max(count, 1), dtype=dtype, device=ids.device)
+
+    local_ids, positions, counts = made(n), made(n), made(shards)
     need = cp_shard_plan_workspace_bytes(n, shards)
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=ids.device)
+    ws = made(need, torch.uint8)
     st = cp_shard_plan(ids.data_ptr(), n, rows_per_shard, shards, local_ids.data_ptr(), positions.data_ptr(),
                        counts.data_ptr(), ws.data_ptr(), ws.numel(), _stream_handle(stream))
     if st != CP_OK:
         raise CPError(st, "cp_shard_plan")
-    for t in (local_ids, positions, counts, ws):
-        _keep_for_stream(t, stream)
     return local_ids[:n], positions[:n], counts[:shards]
 
 
@@ -314,15 +313,21 @@ def _stream_handle(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _keep_for_stream(tensor, stream) -> None:
-    """A tensor allocated here on torch's current stream and used by work on
-    `stream`: tell torch's caching allocator, so the memory is not handed out
-    again before that work is done."""
+def _made_for(stream, make, *shape, dtype, device):
+    """make(*shape) (torch.empty or torch.zeros) for work on `stream`: made on
+    that stream, so that its memory is not in use by work of torch's current
+    stream that `stream` does not wait for, and known to torch's allocator as
+    used by the current stream too, where the caller may drop it."""
     if stream is None:
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    if s != torch.cuda.current_stream():
-        tensor.record_stream(s)
+        return make(*shape, dtype=dtype, device=device)
+    handle, current = _stream_handle(stream), torch.cuda.current_stream(device)
+    if handle == current.cuda_stream:
+        return make(*shape, dtype=dtype, device=device)
+    on = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(on):
+        t = make(*shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
 
 
 class Table:
@@ -360,12 +365,12 @@ class Table:
             raise CPError(st, "cp_table_record_range")
         return off, nb
 
-    def _check_io(self, ids, out, dtype):
+    def _check_io(self, ids, out, dtype, stream):
         if not (ids.is_cuda and ids.dtype == torch.int64 and ids.dim() == 1 and ids.is_contiguous()):
             raise ValueError("ids must be a contiguous 1-D int64 device tensor")
         n = ids.shape[0]
         if out is None:
-            out = torch.empty((n, self.d), dtype=dtype, device=ids.device)
+            out = _made_for(stream, torch.empty, n, self.d, dtype=dtype, device=ids.device)
         if not (out.is_cuda and out.dtype == dtype and tuple(out.shape) == (n, self.d)
                 and out.is_contiguous()):
             raise ValueError(f"out must be a contiguous {dtype} device tensor of shape ({n}, {self.d})")
@@ -373,24 +378,18 @@ class Table:
 
     def lookup_decode(self, ids, out=None, stream=None):
         """bf16[n, d]: alpha * f(c) of rows ids[j], in lookup order."""
-        own = out is None
-        n, out = self._check_io(ids, out, torch.bfloat16)
+        n, out = self._check_io(ids, out, torch.bfloat16, stream)
         st = cp_lookup_decode(self.handle, ids.data_ptr(), n, out.data_ptr(), _stream_handle(stream))
         if st != CP_OK:
             raise CPError(st, "cp_lookup_decode")
-        if own:
-            _keep_for_stream(out, stream)
         return out
 
     def lookup_decode_raw(self, ids, out=None, stream=None):
         """fp16[n, d]: the unscaled f(c) of rows ids[j], in lookup order."""
-        own = out is None
-        n, out = self._check_io(ids, out, torch.float16)
+        n, out = self._check_io(ids, out, torch.float16, stream)
         st = cp_lookup_decode_raw(self.handle, ids.data_ptr(), n, out.data_ptr(), _stream_handle(stream))
         if st != CP_OK:
             raise CPError(st, "cp_lookup_decode_raw")
-        if own:
-            _keep_for_stream(out, stream)
         return out
 
     def dedup_workspace_bytes(self, n: int) -> int:
@@ -401,20 +400,14 @@ class Table:
         workspace: a uint8 device tensor of at least dedup_workspace_bytes(n)
         bytes (allocated here when None); scratch, reusable across calls that
         do not overlap."""
-        own_out = out is None
-        n, out = self._check_io(ids, out, torch.bfloat16)
+        n, out = self._check_io(ids, out, torch.bfloat16, stream)
         need = self.dedup_workspace_bytes(n)
-        own = workspace is None
-        if own:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=ids.device)
+        if workspace is None:
+            workspace = _made_for(stream, torch.empty, max(need, 1), dtype=torch.uint8, device=ids.device)
         st = cp_lookup_decode_dedup(self.handle, ids.data_ptr(), n, out.data_ptr(), workspace.data_ptr(),
                                     workspace.numel() * workspace.element_size(), _stream_handle(stream))
         if st != CP_OK:
             raise CPError(st, "cp_lookup_decode_dedup")
-        if own:
-            _keep_for_stream(workspace, stream)
-        if own_out:
-            _keep_for_stream(out, stream)
         return out
 
     def lookup_decode_dedup_noalloc(self, ids, out, stream=None):
@@ -424,7 +417,7 @@ class Table:
         one device)."""
         if out is None:
             raise ValueError("out must be given (this call allocates nothing)")
-        n, out = self._check_io(ids, out, torch.bfloat16)
+        n, out = self._check_io(ids, out, torch.bfloat16, stream)
         st = cp_lookup_decode_dedup_noalloc(self.handle, ids.data_ptr(), n, out.data_ptr(), _stream_handle(stream))
         if st != CP_OK:
             raise CPError(st, "cp_lookup_decode_dedup_noalloc")
@@ -438,16 +431,13 @@ class Table:
         if not (ids.is_cuda and ids.dtype == torch.int64 and ids.dim() == 1 and ids.is_contiguous()):
             raise ValueError("ids must be a contiguous 1-D int64 device tensor")
         n, R = ids.shape[0], self.record_bytes
-        own = dst is None
-        if own:
-            dst = torch.zeros(n * R + 64, dtype=torch.uint8, device=ids.device)
+        if dst is None:
+            dst = _made_for(stream, torch.zeros, n * R + 64, dtype=torch.uint8, device=ids.device)
         elif not (dst.is_cuda and dst.dtype == torch.uint8 and dst.is_contiguous() and dst.numel() >= n * R):
             raise ValueError(f"dst must be a contiguous uint8 device tensor of at least {n * R} bytes")
         st = cp_table_gather_records(self.handle, ids.data_ptr(), n, dst.data_ptr(), _stream_handle(stream))
         if st != CP_OK:
             raise CPError(st, "cp_table_gather_records")
-        if own:
-            _keep_for_stream(dst, stream)
         return dst
 
     def lookup_decode_staged(self, records, nrecords: int, positions, out=None, stream=None):
@@ -460,14 +450,11 @@ class Table:
                 and records.numel() >= nrecords * R + 64 and records.data_ptr() % 16 == 0):
             raise ValueError("records must be a contiguous, 16-byte aligned uint8 device tensor of at least "
                              f"{nrecords * R + 64} bytes")
-        own = out is None
-        n, out = self._check_io(positions, out, torch.bfloat16)
+        n, out = self._check_io(positions, out, torch.bfloat16, stream)
         st = cp_lookup_decode_staged(self.handle, records.data_ptr(), nrecords, positions.data_ptr(), n,
                                      out.data_ptr(), _stream_handle(stream))
         if st != CP_OK:
             raise CPError(st, "cp_lookup_decode_staged")
-        if own:
-            _keep_for_stream(out, stream)
         return out
 
     def download(self, first_row: int = 0, nrows: int | None = None) -> np.ndarray:
@@ -492,15 +479,12 @@ class Table:
             raise ValueError(f"rows must be a contiguous float32 device tensor of shape (n, {self.d})")
         n = rows.shape[0]
         need = self.encode_workspace_bytes(n)
-        own = workspace is None
-        if own:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=rows.device)
+        if workspace is None:
+            workspace = _made_for(stream, torch.empty, max(need, 1), dtype=torch.uint8, device=rows.device)
         st = cp_table_encode(self.handle, first_row, n, rows.data_ptr(), workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), _stream_handle(stream))
         if st != CP_OK:
             raise CPError(st, "cp_table_encode")
-        if own:
-            _keep_for_stream(workspace, stream)
 
     def set_hot_rows(self, rows) -> int:
         """Keeps device copies of these rows' records (pinned-host tables);
