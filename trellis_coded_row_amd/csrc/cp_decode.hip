@@ -314,7 +314,9 @@ static hipError_t launch_shape(const LaunchArgs &a)
     constexpr int BLOCK = (AHEAD || (KV == 4 && !HOT)) ? kBlockPair : kBlock;
     const uint64_t nchunks = (a.n + CHUNK - 1) / CHUNK;
     uint64_t blocks = (nchunks + BLOCK / 64 - 1) / (BLOCK / 64);
-    if (blocks > 0x7FFFFFFFull) blocks = 0x7FFFFFFFull;  // the chunk loop strides over any excess
+    // a launch of 2^32 threads fails, one of more runs the remainder alone
+    // without an error; the chunk loop strides over any excess
+    if (blocks > 0xFFFFFFFFull / BLOCK) blocks = 0xFFFFFFFFull / BLOCK;
     // workgroups of one residency round
     const uint32_t gen = (uint32_t)(a.num_cus > 0 ? a.num_cus : 256) * (uint32_t)(kBlock / BLOCK);
     hipLaunchKernelGGL((gather_decode<D, KV, RAW, kCopies, BLOCK, CHUNK, HOT, AHEAD>), dim3((unsigned)blocks),

@@ -213,7 +213,9 @@ hipError_t launch_mixed_shape(const MixedLaunchArgs &a)
     constexpr int CHUNK = (CHUNK_ROWS / GROUPS > 0 ? CHUNK_ROWS / GROUPS : 1) * GROUPS;
     const uint64_t nchunks = (a.n + CHUNK - 1) / CHUNK;
     uint64_t blocks = (nchunks + BLOCK / 64 - 1) / (BLOCK / 64);
-    if (blocks > 0x7FFFFFFFull) blocks = 0x7FFFFFFFull;  // the chunk loop strides over any excess
+    // a launch of 2^32 threads fails, one of more runs the remainder alone
+    // without an error; the chunk loop strides over any excess
+    if (blocks > 0xFFFFFFFFull / BLOCK) blocks = 0xFFFFFFFFull / BLOCK;
     hipLaunchKernelGGL((gather_decode_mixed<D, RAW, BLOCK, CHUNK>), dim3((unsigned)blocks), dim3(BLOCK), 0,
                        a.stream, a.records, a.rows, a.lut, a.ids, a.n, a.out, a.err, a.index, a.rates);
     return hipGetLastError();
