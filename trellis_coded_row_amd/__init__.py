@@ -9,7 +9,8 @@ library cannot be loaded, importing this package raises.
 The functions below carry the C names; ``Table`` wraps them for torch
 tensors. ``ops`` (whose names are found here too) holds the dense operators:
 an uncompressed table's lookup and gradient, the norm of looked-up rows, and
-their 8-bit quantiser and product.
+their 8-bit quantiser and product. ``readout`` (its names are found here too)
+holds the readout's product in 16 and 32 bits, its gradients, and dropout.
 """
 from __future__ import annotations
 
@@ -581,3 +582,7 @@ from . import ops as _ops  # noqa: E402
 from .ops import *  # noqa: E402,F401,F403
 
 __all__ += _ops.__all__
+from . import readout as _readout  # noqa: E402
+from .readout import *  # noqa: E402,F401,F403
+
+__all__ += _readout.__all__

@@ -20,17 +20,23 @@ SOURCES = [os.path.join(CSRC, "cp_decode.hip"), os.path.join(CSRC, "cp_dedup.hip
            os.path.join(CSRC, "cp_shard.hip"), os.path.join(CSRC, "cp_dedup_mixed.hip"),
            os.path.join(CSRC, "cp_api.hip"),
            os.path.join(CSRC, "cp_embed.hip"), os.path.join(CSRC, "cp_norm.hip"), os.path.join(CSRC, "cp_quant.hip"),
-           os.path.join(CSRC, "cp_gemm.hip"), os.path.join(CSRC, "cp_ops_api.hip")]
+           os.path.join(CSRC, "cp_gemm.hip"), os.path.join(CSRC, "cp_ops_api.hip"),
+           os.path.join(CSRC, "cp_linear.hip"), os.path.join(CSRC, "cp_linear_dx.hip"),
+           os.path.join(CSRC, "cp_linear_dw.hip"), os.path.join(CSRC, "cp_dropout.hip"),
+           os.path.join(CSRC, "cp_linear_api.hip")]
 DEPS = SOURCES + [os.path.join(CSRC, "cp_internal.h"), os.path.join(CSRC, "cp_lane.h"),
                   os.path.join(CSRC, "cp_encode_copies.h"),
                   os.path.join(CSRC, "cp_status.h"), os.path.join(CSRC, "cp_ops_internal.h"),
-                  os.path.join(ROOT, "include", "cp.h"), os.path.join(ROOT, "include", "cp_ops.h")]
+                  os.path.join(CSRC, "cp_linear_internal.h"), os.path.join(CSRC, "cp_linear_tile.h"),
+                  os.path.join(ROOT, "include", "cp.h"), os.path.join(ROOT, "include", "cp_ops.h"),
+                  os.path.join(ROOT, "include", "cp_linear.h")]
 LIB = os.path.join(PKG, "libcp.so")
 PROBE_SOURCES = [os.path.join(CSRC, "cp_probe.hip")]
 PROBE_LIB = os.path.join(PKG, "libcp_probe.so")
-TORCH_SOURCE = os.path.join(CSRC, "cp_torch.cpp")
+TORCH_SOURCES = [os.path.join(CSRC, "cp_torch.cpp"), os.path.join(CSRC, "cp_torch_linear.cpp")]
 TORCH_LIB = os.path.join(PKG, "_cp_torch.so")
-TORCH_DEPS = [TORCH_SOURCE, os.path.join(ROOT, "include", "cp.h"), os.path.join(ROOT, "include", "cp_ops.h")]
+TORCH_DEPS = TORCH_SOURCES + [os.path.join(CSRC, "cp_torch.h"), os.path.join(ROOT, "include", "cp.h"),
+                              os.path.join(ROOT, "include", "cp_ops.h"), os.path.join(ROOT, "include", "cp_linear.h")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -122,7 +128,7 @@ def build_torch(verbose: bool = False) -> str:
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D__HIP_PLATFORM_AMD__=1",  # what hipcc itself defines; the HIP headers ask for it
            '-DCP_TORCH_MARKS="%s"' % " ".join((_torch_mark(), _source_mark())),
-           *(x for d in include for x in ("-isystem", d)), TORCH_SOURCE, "-o", tmp,
+           *(x for d in include for x in ("-isystem", d)), *TORCH_SOURCES, "-o", tmp,
            "-L", PKG, "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"),
            "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     return _run(cmd, tmp, TORCH_LIB, verbose)

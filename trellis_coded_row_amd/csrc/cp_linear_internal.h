@@ -1,0 +1,202 @@
+// Internal interface of the readout's product, its gradients and dropout
+// (include/cp_linear.h): launch parameters, the mask, the activations and the
+// product's epilogue.
+#pragma once
+
+#include "cp_ops_internal.h"
+
+namespace cpk {
+
+// Activations as in cp_act (include/cp_linear.h).
+enum Act { kNone = 0, kRelu = 1, kGelu = 2, kGeluTanh = 3, kSilu = 4 };
+
+// Dropout of a matrix: threshold 0 keeps everything (rng is not read).
+struct Drop {
+    uint32_t threshold;
+    float scale;
+    const uint64_t *rng;
+};
+
+// What a product's sums become. The residual and both outputs are of the
+// output's type, the bias of the operands'.
+struct Epilogue {
+    const void *bias, *residual;
+    uint64_t residual_stride;
+    void *y, *z;  // z: contiguous
+    uint64_t y_stride;
+    int act;
+    Drop drop;
+};
+
+// out[m][n] = the sum over K of A times B: where an operand is "across", its
+// rows run along K (K x m, K x n), else they are m or n rows of K.
+struct LinearArgs {
+    const void *a, *b;
+    uint64_t a_stride, b_stride;
+    int dtype;
+    uint64_t m, n, k;
+    Epilogue e;
+    uint8_t *workspace;
+    hipStream_t stream;
+};
+uint64_t linear_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int dtype);
+hipError_t linear_rows_by_rows(const LinearArgs &a);      // A, B: rows of K (cp_linear)
+hipError_t linear_rows_by_columns(const LinearArgs &a);   // B across (cp_linear_dx)
+hipError_t linear_columns_by_columns(const LinearArgs &a);  // both across, 32-bit output (cp_linear_dw)
+
+struct ActGradArgs {
+    const void *dy, *z;
+    uint64_t dy_stride, z_stride;
+    int dtype;
+    uint64_t m, n;
+    int act;
+    Drop drop;
+    void *dz;
+    float *db;
+    uint8_t *workspace;
+    hipStream_t stream;
+};
+uint64_t act_grad_workspace_bytes(uint64_t m, uint64_t n);
+hipError_t act_grad(const ActGradArgs &a);
+
+struct DropoutArgs {
+    const void *x, *residual;
+    uint64_t x_stride, residual_stride;
+    int dtype;
+    uint64_t n, d;
+    Drop drop;
+    void *y;
+    hipStream_t stream;
+};
+hipError_t dropout(const DropoutArgs &a);
+
+// ---------------------------------------------------------------- device
+
+// The generator's key and the part of its counter that a launch shares.
+struct Mask {
+    uint32_t key0, key1, offset0, offset1, threshold;
+    float scale;
+};
+
+__device__ __forceinline__ Mask mask_of(const Drop &d)
+{
+    Mask m{};
+    m.threshold = d.threshold;
+    m.scale = d.scale;
+    if (d.threshold) {
+        const uint64_t seed = d.rng[0], offset = d.rng[1];
+        m.key0 = (uint32_t)seed;
+        m.key1 = (uint32_t)(seed >> 32);
+        m.offset0 = (uint32_t)offset;
+        m.offset1 = (uint32_t)(offset >> 32);
+    }
+    return m;
+}
+
+// Philox4x32-10: ten rounds of two 32 x 32-bit products, whose halves change
+// places, with a key that moves by a constant. 20 products of 64 bits for 8
+// values: with 16 bits for each value their time stays below that of the
+// values' own bytes.
+__device__ __forceinline__ u32x4 philox(uint32_t c0, uint32_t c1, const Mask &m)
+{
+    uint32_t c2 = m.offset0, c3 = m.offset1, k0 = m.key0, k1 = m.key1;
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)b;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return u32x4{c0, c1, c2, c3};
+}
+
+// Drops from columns [c, c + 8) of a row (c a multiple of 8).
+__device__ __forceinline__ void drop8(const Mask &m, uint32_t row, uint32_t c, float *f)
+{
+    const u32x4 w = philox(c >> 3, row, m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t half = e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu;
+        f[e] = half >= m.threshold ? f[e] * m.scale : 0.0f;
+    }
+}
+
+// z kept where its functions are at their limits anyway, NaN as it is: an
+// infinity times the 0 it meets would give NaN.
+__device__ __forceinline__ float from_below(float z) { return z < -1e4f ? -1e4f : z; }
+
+__device__ __forceinline__ float within(float z) { return z < -1e4f ? -1e4f : z > 1e4f ? 1e4f : z; }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z)
+{
+    if constexpr (ACT == kRelu) return z < 0.0f ? 0.0f : z;
+    if constexpr (ACT == kGelu) {
+        z = from_below(z);
+        return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    }
+    if constexpr (ACT == kGeluTanh) {
+        z = from_below(z);
+        return z / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+    }
+    if constexpr (ACT == kSilu) {
+        z = from_below(z);
+        return z / (1.0f + expf(-z));
+    }
+    return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z)
+{
+    if constexpr (ACT == kRelu) return z > 0.0f ? 1.0f : 0.0f;
+    z = within(z);
+    if constexpr (ACT == kGelu)
+        return 0.5f * erfcf(-0.70710678118654752f * z) + 0.3989422804014327f * z * expf(-0.5f * z * z);
+    if constexpr (ACT == kGeluTanh) {
+        const float g = 1.0f / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+        return g + z * g * (1.0f - g) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+    }
+    if constexpr (ACT == kSilu) {
+        const float g = 1.0f / (1.0f + expf(-z));
+        return g + z * g * (1.0f - g);
+    }
+    return 1.0f;
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_values(float *f)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = act_value<ACT>(f[e]);
+}
+
+// Sums [c, c + 8) of a row of n (c a multiple of 8) through the epilogue.
+template <int DT, int OUT>
+__device__ __forceinline__ void finish8(const Epilogue &e, const Mask &mask, uint64_t row, uint32_t c, uint32_t n,
+                                        float *f)
+{
+    if (c >= n) return;
+    if (e.bias) {
+        const auto b = load8<DT>((const typename Elem<DT>::raw *)e.bias, c, n);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] += Elem<DT>::get(b[q]);
+    }
+    if (e.z) store8<OUT>((typename Elem<OUT>::raw *)e.z + row * n, c, n, f);
+    if (e.act == kRelu) act_values<kRelu>(f);
+    else if (e.act == kGelu) act_values<kGelu>(f);
+    else if (e.act == kGeluTanh) act_values<kGeluTanh>(f);
+    else if (e.act == kSilu) act_values<kSilu>(f);
+    if (mask.threshold) drop8(mask, (uint32_t)row, c, f);
+    if (e.residual) {
+        const auto r = load8<OUT>((const typename Elem<OUT>::raw *)e.residual + row * e.residual_stride, c, n);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] += Elem<OUT>::get(r[q]);
+    }
+    store8<OUT>((typename Elem<OUT>::raw *)e.y + row * e.y_stride, c, n, f);
+}
+
+}  // namespace cpk

@@ -1,0 +1,509 @@
+// cp_linear_tile.h - the tiled product behind cp_linear, cp_linear_dx and
+// cp_linear_dw: out[m][n] = sum over K of A B, each operand either rows of K or
+// "across" (rows along K), in bf16, f16 or f32, summed in 32 bits.
+#pragma once
+
+#include "cp_linear_internal.h"
+
+namespace cpk {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int unaligned_i32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr uint32_t kStepBytes = 128;         // of each row or column of an operand, per step
+constexpr uint32_t kInside = 0x7FFFFFFFu;    // bytes of a buffer: any offset within a tile
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past it: loads give zeros
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)kInside, 0x00020000);
+}
+
+struct TileParams {
+    const void *a, *b;
+    uint64_t a_stride, b_stride;  // bytes
+    uint32_t m, n, k;
+    uint32_t tiles_m, tiles_n, steps_per_split;
+    float *part;  // the splits' sums, [split][m][n], where k is split
+    Epilogue e;
+};
+
+// A 16-byte piece of each operand: 8 values of K in 16 bits, 4 in 32.
+template <int DT>
+__device__ __forceinline__ f32x16 multiply(i32x4 b, i32x4 a, f32x16 c)
+{
+    if constexpr (DT == kBF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c,
+                                                       0, 0, 0);
+    else if constexpr (DT == kF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0,
+                                                      0, 0);
+    else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__int_as_float(b[e]), __int_as_float(a[e]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+// The same with the accumulator held in one place (16 bits). The s_nop covers
+// the wait that a vector instruction's write to an operand needs, which the
+// compiler does not count for assembly. Results may be read after settle().
+template <int DT>
+__device__ __forceinline__ void multiply_in_place(f32x16 &c, i32x4 b, i32x4 a)
+{
+    static_assert(DT == kBF16 || DT == kF16, "");
+    if constexpr (DT == kBF16)
+        asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+    else
+        asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+a"(c) : "v"(b), "v"(a));
+}
+
+// Waits until the last product's result can be read.
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15"); }
+
+// One operand's tile of W rows (or columns, where it is ACROSS), a step of K
+// at a time, in LDS.
+//
+// Rows of K: a row's 128 bytes are 8 chunks of 16; chunk c of row r stands at
+// c ^ (r / 2 % 8), as a 16-byte LDS read serves 16 lanes at a time, 8 with odd
+// rows and 8 with even ones, which lie in different halves of the banks.
+// ACROSS: a row of the step is the tile's W columns; a read that transposes
+// takes 8 bytes of each of 4 rows for 16 lanes, 32 lanes at a time: 64-byte
+// pieces of 4 rows, which change places within a row so that they lie in
+// different banks. (32-bit columns are read one by one and stay in place.)
+//
+// The copy to LDS writes lane after lane, so the exchange is made in the
+// address that a lane loads from.
+template <int DT, bool ACROSS, int W, int F, bool DIRECT>
+struct Operand {
+    static constexpr uint32_t ES = dtype_bytes(DT), EPC = 16 / ES;  // values of a 16-byte chunk
+    static constexpr uint32_t KS = kStepBytes / ES;                 // values of K in a step
+    static constexpr uint32_t RB = W * ES;                          // bytes of a row in LDS (ACROSS)
+    static constexpr int COPIES = W / 32;                           // of 1 KiB, for each of four waves
+    static constexpr uint32_t BYTES = W * kStepBytes;
+
+    const uint8_t *base;     // of the tile at K = 0
+    uint64_t stride;         // bytes between rows
+    uint32_t from[COPIES];   // byte offset of this lane's chunk of each copy
+    uint32_t at[COPIES];     // its first value's place in K (ACROSS: its row's)
+    uint32_t width;          // ACROSS: the columns from the tile's first on
+    uint32_t read[4];        // where this lane reads its fragments
+    uint32_t w;
+
+    // exchange of 64-byte pieces of row k of a step
+    static __device__ __forceinline__ uint32_t piece(uint32_t k)
+    {
+        if constexpr (ES == 4) return 0;
+        return W >= 128 ? k & 3u : (k >> 1) & 1u;
+    }
+
+    // `first`: the tile's first row or column of `rows`; `part`: which of the
+    // two waves along this operand reads
+    __device__ __forceinline__ Operand(const void *p, uint64_t stride_, uint32_t first, uint32_t rows, uint32_t part)
+    {
+        const uint32_t lane = threadIdx.x & 63u;
+        w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        stride = stride_;
+        width = rows - first;
+        base = (const uint8_t *)p + (ACROSS ? (uint64_t)first * ES : (uint64_t)first * stride);
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+            if constexpr (!ACROSS) {
+                const uint32_t row = (w * COPIES + i) * 8 + (lane >> 3), in = row < width ? row : width - 1;
+                const uint32_t c = ((lane & 7u) ^ ((row >> 1) & 7u)) * 16;
+                from[i] = in * (uint32_t)stride + c;
+                at[i] = c / ES;
+            } else {
+                const uint32_t o = (w * COPIES + i) * 1024 + lane * 16, row = o / RB, in = o % RB;
+                const uint32_t c = (((in / 64) ^ piece(row)) * 64 + in % 64) / ES;
+                // past the last column: the last chunk (DIRECT: columns are whole chunks)
+                from[i] = row * (uint32_t)stride + (DIRECT && c >= width ? width - EPC : c) * ES;
+                at[i] = row;
+            }
+        }
+        const uint32_t r = lane & 31u, h = lane >> 5;
+        if constexpr (!ACROSS) {
+            const uint32_t o = (part * F * 32 + r) * kStepBytes + (h ^ ((r >> 1) & 7u)) * 16;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) read[q] = o ^ (q * 32);
+        } else if constexpr (ES == 2) {
+            const uint32_t j = (lane & 15u) >> 2, g = lane & 3u, b = (lane >> 4) & 1u;
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+                read[i] = (8 * h + j) * RB + (((part * F + i) ^ piece(j)) * 64) + 32 * b + 8 * g;
+        } else {
+            read[0] = 4 * h * RB + (part * F * 32 + r) * 4;
+        }
+    }
+
+    // copy i of the step at K = k0 of k
+    __device__ __forceinline__ void copy(uint8_t *lds, int i, uint32_t k0, uint32_t k) const
+    {
+        static_assert(DIRECT, "");
+        const auto rsrc = buffer_of(base + (ACROSS ? (uint64_t)k0 * stride : (uint64_t)k0 * ES));
+        const uint32_t v = at[i] < k - k0 ? from[i] : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(lds + (w * COPIES + i) * 1024), 16, v, 0, 0, 0);
+    }
+
+    // The same by way of a register, for rows at any alignment: values past
+    // the end of K or of a row are zeros.
+    __device__ __forceinline__ i32x4 load(int i, uint32_t k0, uint32_t k) const
+    {
+        typedef typename Elem<DT>::raw raw;
+        const raw *const row = (const raw *)(base + (ACROSS ? (uint64_t)k0 * stride : (uint64_t)k0 * ES) + from[i]);
+        i32x4 v = {0, 0, 0, 0};
+        uint32_t have;  // values from the chunk's first on
+        if constexpr (ACROSS) {
+            const uint32_t lane = threadIdx.x & 63u, in = ((w * COPIES + i) * 1024 + lane * 16) % RB;
+            const uint32_t c = (((in / 64) ^ piece(at[i])) * 64 + in % 64) / ES;
+            have = at[i] < k - k0 && c < width ? width - c : 0;
+        } else {
+            have = at[i] < k - k0 ? k - k0 - at[i] : 0;
+        }
+        if (have >= EPC) {
+            v = *reinterpret_cast<const unaligned_i32x4 *>(row);
+        } else if (have) {
+            raw e[EPC] = {};
+#pragma unroll
+            for (uint32_t q = 0; q < EPC; ++q)
+                if (q < have) e[q] = row[q];
+            __builtin_memcpy(&v, e, 16);
+        }
+        return v;
+    }
+
+    __device__ __forceinline__ void put(uint8_t *lds, int i, i32x4 v) const
+    {
+        *reinterpret_cast<i32x4 *>(lds + (w * COPIES + i) * 1024 + (threadIdx.x & 63u) * 16) = v;
+    }
+
+    // fragment i of quarter q of the step: lane l has row (or column) l % 32,
+    // the chunk 2 q + l / 32 of it
+    __device__ __forceinline__ i32x4 fragment(const uint8_t *lds, int q, int i) const
+    {
+        if constexpr (!ACROSS) {
+            return *reinterpret_cast<const i32x4 *>(lds + read[q] + i * 32 * kStepBytes);
+        } else if constexpr (ES == 2) {
+            const uint8_t *const from_ = lds + read[i] + q * 16 * RB;
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(from_));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(from_ + 4 * RB));
+            return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            i32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const int *>(lds + read[0] + (q * 8 + e) * RB + i * 128);
+            return v;
+        }
+    }
+};
+
+// A workgroup's tile and its steps of K.
+struct TilePlace {
+    uint32_t m0, n0, split, s0, s1;
+};
+
+// Each of the 8 XCDs (workgroup ids taken in turn) gets a contiguous run of
+// tiles, which go down 8 tile rows at a time, so that the operands an XCD
+// reads at one time are few enough for its own L2.
+__device__ __forceinline__ TilePlace place_of(const TileParams &p, uint32_t BM, uint32_t BN, uint32_t ks)
+{
+    const uint32_t ntiles = p.tiles_m * p.tiles_n, total = gridDim.x;
+    const uint32_t xcd = blockIdx.x & 7u, per = total >> 3, extra = total & 7u;
+    const uint32_t id = xcd * per + (xcd < extra ? xcd : extra) + (blockIdx.x >> 3);
+    // (the quotients come out of vector registers: back to scalar ones)
+    const uint32_t split = __builtin_amdgcn_readfirstlane(id / ntiles), tile = id - split * ntiles;
+    const uint32_t band = __builtin_amdgcn_readfirstlane(tile / (8 * p.tiles_n)), band_m = band * 8;
+    const uint32_t band_rows = p.tiles_m - band_m < 8 ? p.tiles_m - band_m : 8;
+    const uint32_t in_band = tile - band * 8 * p.tiles_n;
+    const uint32_t column = __builtin_amdgcn_readfirstlane(in_band / band_rows);
+    TilePlace t;
+    t.m0 = (band_m + in_band - column * band_rows) * BM;
+    t.n0 = column * BN;
+    const uint32_t all = (p.k + ks - 1) / ks;
+    t.split = split;
+    t.s0 = split * p.steps_per_split;
+    t.s1 = t.s0 + p.steps_per_split < all ? t.s0 + p.steps_per_split : all;
+    return t;
+}
+
+// Tiles of 64 FM x 64 FN outputs; four waves, 2 x 2, each with FM x FN
+// fragments of 32 x 32. B's columns are the instruction's rows, so that a lane
+// holds 4 neighbours of an output row (row l % 32, columns 8 a + 4 (l / 32) +
+// 0 .. 3 for a < 4). A step's operands are copied to LDS by loads that bypass
+// the registers, one step ahead, into the other of two buffers. One barrier
+// per step, before its last quarter is multiplied: by then every wave has
+// read all it needs of this step and its own copies of the next have landed.
+//
+// DIRECT needs both operands' rows to start on 16 bytes and to be whole
+// chunks of 16 along their rows; others come by way of registers.
+template <int DT, bool AX, bool BX, int OUT, int FM, int FN, bool DIRECT>
+__global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void linear_tile(TileParams p)
+{
+    constexpr int BM = 64 * FM, BN = 64 * FN;
+    typedef Operand<DT, AX, BM, FM, DIRECT> OpA;
+    typedef Operand<DT, BX, BN, FN, DIRECT> OpB;
+    constexpr bool IN_PLACE = FM * FN == 16;
+    constexpr uint32_t KS = OpA::KS;
+    // an epilogue's slab of 32 rows of a wave has its place in one of them
+    constexpr uint32_t SLAB_ROW = FN * 128 + 16;
+    __shared__ __attribute__((aligned(16))) uint8_t as0[OpA::BYTES], as1[OpA::BYTES], bs0[OpB::BYTES], bs1[OpB::BYTES];
+    static_assert(FM == FN && 32 * SLAB_ROW <= OpA::BYTES, "");
+    const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t wm = w >> 1, wn = w & 1u;
+    const TilePlace place = place_of(p, BM, BN, KS);
+    const uint32_t s1 = place.s1;
+    const OpA A(p.a, p.a_stride, place.m0, p.m, wm);
+    const OpB B(p.b, p.b_stride, place.n0, p.n, wn);
+
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int f = 0; f < FN; ++f) acc[i][f] = (f32x16)0.0f;
+    i32x4 a[2][FM], b[2][FN];
+    [[maybe_unused]] i32x4 ra[OpA::COPIES], rb[OpB::COPIES];
+
+    const auto read = [&](const uint8_t *as, const uint8_t *bs, int q, int into) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) a[into][i] = A.fragment(as, q, i);
+#pragma unroll
+        for (int f = 0; f < FN; ++f) b[into][f] = B.fragment(bs, q, f);
+    };
+    // step s, whose operands are in (as, bs); the next one's go to (an, bn)
+    const auto step = [&](uint32_t s, uint8_t *as, uint8_t *bs, uint8_t *an, uint8_t *bn) {
+        if constexpr (!DIRECT) {
+            if (s + 1 < s1) {
+#pragma unroll
+                for (int i = 0; i < OpA::COPIES; ++i) ra[i] = A.load(i, (s + 1) * KS, p.k);
+#pragma unroll
+                for (int i = 0; i < OpB::COPIES; ++i) rb[i] = B.load(i, (s + 1) * KS, p.k);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int cur = q & 1;
+            if (q < 3) {
+                read(as, bs, q + 1, cur ^ 1);
+            } else {
+                if constexpr (!DIRECT) {
+                    if (s + 1 < s1) {
+#pragma unroll
+                        for (int i = 0; i < OpA::COPIES; ++i) A.put(an, i, ra[i]);
+#pragma unroll
+                        for (int i = 0; i < OpB::COPIES; ++i) B.put(bn, i, rb[i]);
+                    }
+                }
+                __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's LDS accesses and copies are done
+                __syncthreads();
+                if (s + 1 < s1) read(an, bn, 0, cur ^ 1);
+            }
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                if constexpr (DIRECT) {
+                    if (q == 0 && s + 1 < s1) {
+#pragma unroll
+                        for (int i = 0; i < OpB::COPIES / FN; ++i) B.copy(bn, f * (OpB::COPIES / FN) + i, (s + 1) * KS, p.k);
+                    }
+                    if (q == 3 && s + 2 < s1) {
+#pragma unroll
+                        for (int i = 0; i < OpA::COPIES / FN; ++i) A.copy(as, f * (OpA::COPIES / FN) + i, (s + 2) * KS, p.k);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    if constexpr (IN_PLACE) multiply_in_place<DT>(acc[i][f], b[cur][f], a[cur][i]);
+                    else acc[i][f] = multiply<DT>(b[cur][f], a[cur][i], acc[i][f]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+
+    uint32_t s = place.s0;
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int i = 0; i < OpA::COPIES; ++i) A.copy(as0, i, s * KS, p.k);
+#pragma unroll
+        for (int i = 0; i < OpB::COPIES; ++i) B.copy(bs0, i, s * KS, p.k);
+        if (s + 1 < s1) {
+#pragma unroll
+            for (int i = 0; i < OpA::COPIES; ++i) A.copy(as1, i, (s + 1) * KS, p.k);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < OpA::COPIES; ++i) A.put(as0, i, A.load(i, s * KS, p.k));
+#pragma unroll
+        for (int i = 0; i < OpB::COPIES; ++i) B.put(bs0, i, B.load(i, s * KS, p.k));
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __syncthreads();
+    read(as0, bs0, 0, 0);
+    do {
+        step(s, as0, bs0, as1, bs1);
+        if (++s == s1) break;
+        step(s, as1, bs1, as0, bs0);
+    } while (++s < s1);
+    __syncthreads();  // every wave's last reads are done
+
+    if constexpr (IN_PLACE) {
+        settle();
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int f = 0; f < FN; ++f) asm volatile("" : "+a"(acc[i][f]));
+    }
+    // by way of LDS, so that 8 neighbours meet in a lane and rows are written
+    // in long pieces
+    uint8_t *const slab = w == 0 ? as0 : w == 1 ? as1 : w == 2 ? bs0 : bs1;
+    const Mask mask = mask_of(p.part ? Drop{} : p.e.drop);
+    constexpr uint32_t GROUPS = 4 * FN, ROWS = 64 / GROUPS;  // groups of 8 in a slab's row; rows at a time
+    const uint32_t r = lane & 31u, h = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4 *>(slab + r * SLAB_ROW + (32 * f + 8 * q + 4 * h) * 4) =
+                    f32x4{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (a wave's own: its LDS accesses stay in order)
+#pragma unroll 1
+        for (uint32_t t = 0; t < 32 / ROWS; ++t) {
+            const uint32_t row = t * ROWS + lane / GROUPS, group = lane % GROUPS;
+            float o[8];
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(slab + row * SLAB_ROW + group * 32);
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(slab + row * SLAB_ROW + group * 32 + 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                o[e] = lo[e];
+                o[4 + e] = hi[e];
+            }
+            const uint32_t m = place.m0 + (wm * FM + i) * 32 + row, n = place.n0 + wn * FN * 32 + group * 8;
+            if (m < p.m && n < p.n) {
+                if (p.part) store8<kF32>(p.part + ((uint64_t)place.split * p.m + m) * p.n, n, p.n, o);
+                else finish8<DT, OUT>(p.e, mask, m, n, p.n, o);
+            }
+        }
+        asm volatile("" ::: "memory");
+    }
+}
+
+// The splits' sums, joined in order, through the epilogue (none: zeros).
+template <int DT, int OUT>
+__global__ __launch_bounds__(256) void join_parts(const float *__restrict__ part, uint32_t splits, uint32_t n8,
+                                                  uint32_t m, uint32_t n, Epilogue e)
+{
+    const Mask mask = mask_of(e.drop);
+    const uint64_t count = (uint64_t)m * n8;
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (uint64_t)gridDim.x * 256) {
+        const uint32_t row = (uint32_t)(i / n8), c = (uint32_t)(i - (uint64_t)row * n8) * 8;
+        float f[8] = {};
+        for (uint32_t s = 0; s < splits; ++s) {
+            const auto v = load8<kF32>(part + ((uint64_t)s * m + row) * n, c, n);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[q] += v[q];
+        }
+        finish8<DT, OUT>(e, mask, row, c, n, f);
+    }
+}
+
+// How a product is cut: tiles of 64 f x 64 f, and splits of K.
+struct Cut {
+    int f;
+    uint32_t splits, steps_per_split;
+};
+
+Cut cut_of(uint64_t m, uint64_t n, uint64_t k, int dtype, bool direct)
+{
+    const uint32_t steps = (uint32_t)div_up(k * dtype_bytes(dtype), kStepBytes);
+    struct Kind { int f; double step, ends; uint32_t per_cu; };
+    static const Kind narrow[] = {{4, 2400, 6000, 1}, {2, 900, 4000, 2}, {1, 330, 3000, 4}};
+    static const Kind wide[] = {{4, 16400, 6000, 1}, {2, 4200, 4000, 2}, {1, 1100, 3000, 4}};
+    const Kind *const kinds = dtype == kF32 ? wide : narrow;
+    Cut best{};
+    double least = 0;
+    for (int q = 0; q < 3; ++q) {
+        const Kind &t = kinds[q];
+        if (t.f == 4 && (dtype == kF32 || !direct)) continue;
+        const uint64_t tiles = div_up(m, 64u * t.f) * div_up(n, 64u * t.f);
+        for (uint32_t want = 1; want <= 16; want *= 2) {
+            const uint32_t per = (uint32_t)div_up(steps, want), splits = (uint32_t)div_up(steps, per);
+            if (want > 1 && (per < 8 || splits != want)) continue;
+            const uint64_t wgs = tiles * splits;
+            if (wgs >= (1u << 24)) continue;  // a launch has fewer than 2^32 threads
+            const uint64_t full = wgs / (256 * t.per_cu), rest = wgs % (256 * t.per_cu);
+            const double share = rest ? (double)div_up(rest, 256) : 0;
+            double cost = (full * t.per_cu + share) * per * t.step + (full + (rest ? 1 : 0)) * t.ends;
+            if (splits > 1) cost += 6000 + (double)m * n * 4 * (splits + 1) / 2000;
+            if (best.f == 0 || cost < least) {
+                least = cost;
+                best = Cut{t.f, splits, per};
+            }
+        }
+    }
+    return best;
+}
+
+inline uint64_t workspace_of(const Cut &c, uint64_t m, uint64_t n) { return c.splits > 1 ? 4ull * c.splits * m * n : 0; }
+
+template <int DT, int OUT>
+hipError_t join(const LinearArgs &g, uint32_t splits)
+{
+    const uint64_t n8 = div_up(g.n, 8), wgs = div_up(g.m * n8, 256);
+    join_parts<DT, OUT><<<(uint32_t)(wgs < 8192 ? wgs : 8192), 256, 0, g.stream>>>(
+        (const float *)g.workspace, splits, (uint32_t)n8, (uint32_t)g.m, (uint32_t)g.n, g.e);
+    return hipGetLastError();
+}
+
+// Whether an operand's rows can be copied to LDS in chunks of 16 bytes.
+inline bool whole_chunks(const void *p, uint64_t stride_bytes, uint64_t row_bytes)
+{
+    return ((uintptr_t)p | stride_bytes | row_bytes) % 16 == 0;
+}
+
+template <int DT, bool AX, bool BX, int OUT>
+hipError_t launch_linear(const LinearArgs &g)
+{
+    if (g.k == 0) return join<DT, OUT>(g, 0);
+    constexpr uint64_t es = dtype_bytes(DT);
+    const bool direct = whole_chunks(g.a, g.a_stride * es, (AX ? g.m : g.k) * es) &&
+                        whole_chunks(g.b, g.b_stride * es, (BX ? g.n : g.k) * es);
+    const Cut c = cut_of(g.m, g.n, g.k, DT, direct);
+    TileParams p{};
+    p.a = g.a;
+    p.b = g.b;
+    p.a_stride = g.a_stride * es;
+    p.b_stride = g.b_stride * es;
+    p.m = (uint32_t)g.m;
+    p.n = (uint32_t)g.n;
+    p.k = (uint32_t)g.k;
+    p.tiles_m = (uint32_t)div_up(g.m, 64u * c.f);
+    p.tiles_n = (uint32_t)div_up(g.n, 64u * c.f);
+    p.steps_per_split = c.steps_per_split;
+    p.part = c.splits > 1 ? (float *)g.workspace : nullptr;
+    p.e = g.e;
+    const uint32_t blocks = p.tiles_m * p.tiles_n * c.splits;
+    if (direct) {
+        if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, true><<<blocks, 256, 0, g.stream>>>(p);
+        else if (c.f == 2) linear_tile<DT, AX, BX, OUT, 2, 2, true><<<blocks, 256, 0, g.stream>>>(p);
+        else if constexpr (DT != kF32) linear_tile<DT, AX, BX, OUT, 4, 4, true><<<blocks, 256, 0, g.stream>>>(p);
+    } else {
+        if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, false><<<blocks, 256, 0, g.stream>>>(p);
+        else linear_tile<DT, AX, BX, OUT, 2, 2, false><<<blocks, 256, 0, g.stream>>>(p);
+    }
+    if (c.splits > 1) return join<DT, OUT>(g, c.splits);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace cpk

@@ -64,7 +64,7 @@ def _bind(name: str, res, *args):
     return fn
 
 
-_vp, _u64, _int, _f32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int, ctypes.c_float
+_vp, _u64, _int, _f32, _f64 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int, ctypes.c_float, ctypes.c_double
 
 cp_embed_lookup = _bind("cp_embed_lookup", _int, _vp, _int, _u64, _u64, _u64, _vp, _u64, _f32, _vp, _int, _vp, _vp)
 cp_embed_plan_workspace_bytes = _bind("cp_embed_plan_workspace_bytes", _u64, _u64, _u64)
