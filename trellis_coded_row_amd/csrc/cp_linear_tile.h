@@ -22,9 +22,9 @@ constexpr uint32_t kStepBytes = 128;         // of each row or column of an oper
 constexpr uint32_t kInside = 0x7FFFFFFFu;    // bytes of a buffer: any offset within a tile
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past it: loads give zeros
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t size)
 {
-    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)kInside, 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)size, 0x00020000);
 }
 
 struct TileParams {
@@ -145,11 +145,11 @@ struct Operand {
         }
     }
 
-    // copy i of the step at K = k0 of k
+    // copy i of the step at K = k0; zeros from k on
     __device__ __forceinline__ void copy(uint8_t *lds, int i, uint32_t k0, uint32_t k) const
     {
         static_assert(DIRECT, "");
-        const auto rsrc = buffer_of(base + (ACROSS ? (uint64_t)k0 * stride : (uint64_t)k0 * ES));
+        const auto rsrc = buffer_of(base + (ACROSS ? (uint64_t)k0 * stride : (uint64_t)k0 * ES), k0 < k ? kInside : 0);
         const uint32_t v = at[i] < k - k0 ? from[i] : kOutside;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(lds + (w * COPIES + i) * 1024), 16, v, 0, 0, 0);
     }
@@ -165,9 +165,9 @@ struct Operand {
         if constexpr (ACROSS) {
             const uint32_t lane = threadIdx.x & 63u, in = ((w * COPIES + i) * 1024 + lane * 16) % RB;
             const uint32_t c = (((in / 64) ^ piece(at[i])) * 64 + in % 64) / ES;
-            have = at[i] < k - k0 && c < width ? width - c : 0;
+            have = k0 + at[i] < k && c < width ? width - c : 0;
         } else {
-            have = at[i] < k - k0 ? k - k0 - at[i] : 0;
+            have = k0 + at[i] < k ? k - k0 - at[i] : 0;
         }
         if (have >= EPC) {
             v = *reinterpret_cast<const unaligned_i32x4 *>(row);
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void l
     const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t wm = w >> 1, wn = w & 1u;
     const TilePlace place = place_of(p, BM, BN, KS);
-    const uint32_t s1 = place.s1;
+    const uint32_t s1 = place.s1, end = s1 * KS < p.k ? s1 * KS : p.k;  // of this split's part of K
     const OpA A(p.a, p.a_stride, place.m0, p.m, wm);
     const OpB B(p.b, p.b_stride, place.n0, p.n, wn);
 
@@ -278,15 +278,14 @@ __global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void l
 #pragma unroll
         for (int f = 0; f < FN; ++f) b[into][f] = B.fragment(bs, q, f);
     };
-    // step s, whose operands are in (as, bs); the next one's go to (an, bn)
+    // step s, whose operands are in (as, bs); the next one's go to (an, bn).
+    // Past the last step there are zeros.
     const auto step = [&](uint32_t s, uint8_t *as, uint8_t *bs, uint8_t *an, uint8_t *bn) {
         if constexpr (!DIRECT) {
-            if (s + 1 < s1) {
 #pragma unroll
-                for (int i = 0; i < OpA::COPIES; ++i) ra[i] = A.load(i, (s + 1) * KS, p.k);
+            for (int i = 0; i < OpA::COPIES; ++i) ra[i] = A.load(i, (s + 1) * KS, end);
 #pragma unroll
-                for (int i = 0; i < OpB::COPIES; ++i) rb[i] = B.load(i, (s + 1) * KS, p.k);
-            }
+            for (int i = 0; i < OpB::COPIES; ++i) rb[i] = B.load(i, (s + 1) * KS, end);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -295,27 +294,25 @@ __global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void l
                 read(as, bs, q + 1, cur ^ 1);
             } else {
                 if constexpr (!DIRECT) {
-                    if (s + 1 < s1) {
 #pragma unroll
-                        for (int i = 0; i < OpA::COPIES; ++i) A.put(an, i, ra[i]);
+                    for (int i = 0; i < OpA::COPIES; ++i) A.put(an, i, ra[i]);
 #pragma unroll
-                        for (int i = 0; i < OpB::COPIES; ++i) B.put(bn, i, rb[i]);
-                    }
+                    for (int i = 0; i < OpB::COPIES; ++i) B.put(bn, i, rb[i]);
                 }
                 __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's LDS accesses and copies are done
                 __syncthreads();
-                if (s + 1 < s1) read(an, bn, 0, cur ^ 1);
+                read(an, bn, 0, cur ^ 1);
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
                 if constexpr (DIRECT) {
-                    if (q == 0 && s + 1 < s1) {
+                    if (q == 0) {
 #pragma unroll
-                        for (int i = 0; i < OpB::COPIES / FN; ++i) B.copy(bn, f * (OpB::COPIES / FN) + i, (s + 1) * KS, p.k);
+                        for (int i = 0; i < OpB::COPIES / FN; ++i) B.copy(bn, f * (OpB::COPIES / FN) + i, (s + 1) * KS, end);
                     }
-                    if (q == 3 && s + 2 < s1) {
+                    if (q == 3) {
 #pragma unroll
-                        for (int i = 0; i < OpA::COPIES / FN; ++i) A.copy(as, f * (OpA::COPIES / FN) + i, (s + 2) * KS, p.k);
+                        for (int i = 0; i < OpA::COPIES / FN; ++i) A.copy(as, f * (OpA::COPIES / FN) + i, (s + 2) * KS, end);
                     }
                 }
 #pragma unroll
@@ -331,28 +328,28 @@ __global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void l
     uint32_t s = place.s0;
     if constexpr (DIRECT) {
 #pragma unroll
-        for (int i = 0; i < OpA::COPIES; ++i) A.copy(as0, i, s * KS, p.k);
+        for (int i = 0; i < OpA::COPIES; ++i) A.copy(as0, i, s * KS, end);
 #pragma unroll
-        for (int i = 0; i < OpB::COPIES; ++i) B.copy(bs0, i, s * KS, p.k);
-        if (s + 1 < s1) {
+        for (int i = 0; i < OpB::COPIES; ++i) B.copy(bs0, i, s * KS, end);
 #pragma unroll
-            for (int i = 0; i < OpA::COPIES; ++i) A.copy(as1, i, (s + 1) * KS, p.k);
-        }
+        for (int i = 0; i < OpA::COPIES; ++i) A.copy(as1, i, (s + 1) * KS, end);
     } else {
 #pragma unroll
-        for (int i = 0; i < OpA::COPIES; ++i) A.put(as0, i, A.load(i, s * KS, p.k));
+        for (int i = 0; i < OpA::COPIES; ++i) A.put(as0, i, A.load(i, s * KS, end));
 #pragma unroll
-        for (int i = 0; i < OpB::COPIES; ++i) B.put(bs0, i, B.load(i, s * KS, p.k));
+        for (int i = 0; i < OpB::COPIES; ++i) B.put(bs0, i, B.load(i, s * KS, end));
     }
     __builtin_amdgcn_s_waitcnt(0x0070);
     __syncthreads();
     read(as0, bs0, 0, 0);
+    // two steps a turn, the second of an odd number on zeros
     do {
         step(s, as0, bs0, as1, bs1);
-        if (++s == s1) break;
-        step(s, as1, bs1, as0, bs0);
-    } while (++s < s1);
-    __syncthreads();  // every wave's last reads are done
+        step(s + 1, as1, bs1, as0, bs0);
+        s += 2;
+    } while (s < s1);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // the copies past the end (zeros) are in LDS
+    __syncthreads();                     // and every wave's last reads are done
 
     if constexpr (IN_PLACE) {
         settle();
