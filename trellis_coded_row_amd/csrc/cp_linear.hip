@@ -128,7 +128,11 @@ __global__ __launch_bounds__(kRowWaves * 64, 2) void linear_rows(RowsParams p)
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] += sums[q][row][c + e];
     if (p.part) store8<kF32>(p.part + ((uint64_t)split * p.m + row) * p.n, n0 + c, p.n, f);
-    else finish8<DT, DT>(p.e, mask_of(p.e.drop), row, n0 + c, p.n, f);
+    else {
+        float bias[8];
+        bias8<DT>(p.e, n0 + c, p.n, bias);
+        finish8<DT>(p.e, mask_of(p.e.drop), row, n0 + c, p.n, f, bias, residual8<DT>(p.e, row, n0 + c, p.n));
+    }
 }
 
 constexpr uint64_t kFewRows = 32;
@@ -170,9 +174,12 @@ hipError_t launch_rows(const LinearArgs &g)
 
 uint64_t linear_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int dtype)
 {
-    const uint64_t a = workspace_of(cut_of(m, n, k, dtype, true), m, n), b = workspace_of(cut_of(m, n, k, dtype, false), m, n);
-    const uint64_t c = m <= kFewRows ? workspace_of(rows_cut(n, k, dtype), m, n) : 0;
-    return a > b ? (a > c ? a : c) : (b > c ? b : c);
+    uint64_t most = m <= kFewRows ? workspace_of(rows_cut(n, k, dtype), m, n) : 0;
+    for (Rows rows : {kWhole, kOdd, kShort}) {
+        const uint64_t bytes = workspace_of(cut_of(m, n, k, dtype, rows), m, n);
+        most = bytes > most ? bytes : most;
+    }
+    return most;
 }
 
 template <int DT>

@@ -3,6 +3,11 @@
 // "across" (rows along K), in bf16, f16 or f32, summed in 32 bits.
 #pragma once
 
+#include <type_traits>
+#ifdef SWEEP
+#include <stdlib.h>
+#endif
+
 #include "cp_linear_internal.h"
 
 namespace cpk {
@@ -85,6 +90,7 @@ __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15");
 // address that a lane loads from.
 template <int DT, bool ACROSS, int W, int F, bool DIRECT>
 struct Operand {
+    static constexpr bool SHORT = F == 1;  // rows of less than a chunk are read too
     static constexpr uint32_t ES = dtype_bytes(DT), EPC = 16 / ES;  // values of a 16-byte chunk
     static constexpr uint32_t KS = kStepBytes / ES;                 // values of K in a step
     static constexpr uint32_t RB = W * ES;                          // bytes of a row in LDS (ACROSS)
@@ -93,7 +99,7 @@ struct Operand {
 
     const uint8_t *base;     // of the tile at K = 0
     uint64_t stride;         // bytes between rows
-    uint32_t from[COPIES];   // byte offset of this lane's chunk of each copy
+    uint32_t from[COPIES];   // byte offset of this lane's chunk of each copy (its row, where not DIRECT; not of ACROSS then)
     uint32_t at[COPIES];     // its first value's place in K (ACROSS: its row's)
     uint32_t width;          // ACROSS: the columns from the tile's first on
     uint32_t read[4];        // where this lane reads its fragments
@@ -120,14 +126,13 @@ struct Operand {
             if constexpr (!ACROSS) {
                 const uint32_t row = (w * COPIES + i) * 8 + (lane >> 3), in = row < width ? row : width - 1;
                 const uint32_t c = ((lane & 7u) ^ ((row >> 1) & 7u)) * 16;
-                from[i] = in * (uint32_t)stride + c;
+                from[i] = in * (uint32_t)stride + (DIRECT ? c : 0);
                 at[i] = c / ES;
             } else {
-                const uint32_t o = (w * COPIES + i) * 1024 + lane * 16, row = o / RB, in = o % RB;
-                const uint32_t c = (((in / 64) ^ piece(row)) * 64 + in % 64) / ES;
+                at[i] = ((w * COPIES + i) * 1024 + lane * 16) / RB;
+                const uint32_t c = column(i);
                 // past the last column: the last chunk (DIRECT: columns are whole chunks)
-                from[i] = row * (uint32_t)stride + (DIRECT && c >= width ? width - EPC : c) * ES;
-                at[i] = row;
+                if constexpr (DIRECT) from[i] = at[i] * (uint32_t)stride + (c >= width ? width - EPC : c) * ES;
             }
         }
         const uint32_t r = lane & 31u, h = lane >> 5;
@@ -145,40 +150,72 @@ struct Operand {
         }
     }
 
-    // copy i of the step at K = k0; zeros from k on
+    // copy i of the step at K = k0; zeros from k on (DIRECT)
     __device__ __forceinline__ void copy(uint8_t *lds, int i, uint32_t k0, uint32_t k) const
     {
-        static_assert(DIRECT, "");
         const auto rsrc = buffer_of(base + (ACROSS ? (uint64_t)k0 * stride : (uint64_t)k0 * ES), k0 < k ? kInside : 0);
         const uint32_t v = at[i] < k - k0 ? from[i] : kOutside;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(lds + (w * COPIES + i) * 1024), 16, v, 0, 0, 0);
     }
 
-    // The same by way of a register, for rows at any alignment: values past
-    // the end of K or of a row are zeros.
-    __device__ __forceinline__ i32x4 load(int i, uint32_t k0, uint32_t k) const
+    // The same by way of a register, for rows at any alignment (of at least a
+    // chunk, where not SHORT): a chunk that
+    // reaches past the end of its row is read from the row's last 16 bytes
+    // and moved into place by fix(), which has to be called where may_reach()
+    // says so. `end` is at least 1.
+    __device__ __forceinline__ i32x4 load(int i, uint32_t k0, uint32_t end) const
     {
-        typedef typename Elem<DT>::raw raw;
-        const raw *const row = (const raw *)(base + (ACROSS ? (uint64_t)k0 * stride : (uint64_t)k0 * ES) + from[i]);
-        i32x4 v = {0, 0, 0, 0};
-        uint32_t have;  // values from the chunk's first on
         if constexpr (ACROSS) {
-            const uint32_t lane = threadIdx.x & 63u, in = ((w * COPIES + i) * 1024 + lane * 16) % RB;
-            const uint32_t c = (((in / 64) ^ piece(at[i])) * 64 + in % 64) / ES;
-            have = k0 + at[i] < k && c < width ? width - c : 0;
+            const uint32_t first = k0 < end ? k0 : end - 1, last = end - 1 - first;  // (rows past the end: the last one)
+            const uint32_t row = at[i] < last ? at[i] : last, c = column(i), most = width - EPC;
+            const uint8_t *const p = base + (uint64_t)first * stride;
+            const uint32_t o = (__umul24(row, (uint32_t)stride / ES) + ((!SHORT || width >= EPC) && c > most ? most : c)) * ES;
+            return SHORT && width < EPC ? piecewise(p + o, row == at[i] && k0 < end && c < width ? width - c : 0)
+                               : *reinterpret_cast<const unaligned_i32x4 *>(p + o);
         } else {
-            have = k0 + at[i] < k ? k - k0 - at[i] : 0;
+            const uint32_t c = k0 + at[i], most = end - EPC;
+            return SHORT && end < EPC ? piecewise(base + from[i] + c * ES, c < end ? end - c : 0)
+                             : *reinterpret_cast<const unaligned_i32x4 *>(base + (from[i] + (c < most ? c : most) * ES));
         }
-        if (have >= EPC) {
-            v = *reinterpret_cast<const unaligned_i32x4 *>(row);
-        } else if (have) {
-            raw e[EPC] = {};
+    }
+
+    // `have` values of a chunk
+    static __device__ __forceinline__ i32x4 piecewise(const uint8_t *p, uint32_t have)
+    {
+        typename Elem<DT>::raw e[EPC] = {};
 #pragma unroll
-            for (uint32_t q = 0; q < EPC; ++q)
-                if (q < have) e[q] = row[q];
-            __builtin_memcpy(&v, e, 16);
-        }
+        for (uint32_t q = 0; q < EPC; ++q)
+            if (q < have) e[q] = ((const typename Elem<DT>::raw *)p)[q];
+        i32x4 v;
+        __builtin_memcpy(&v, e, 16);
         return v;
+    }
+
+    // ACROSS: the column of this lane's chunk of copy i
+    __device__ __forceinline__ uint32_t column(int i) const
+    {
+        const uint32_t in = ((w * COPIES + i) * 1024 + (threadIdx.x & 63u) * 16) % RB;
+        return (((in / 64) ^ piece(at[i])) * 64 + in % 64) / ES;
+    }
+
+    __device__ __forceinline__ bool may_reach(uint32_t k0, uint32_t end) const
+    {
+        return k0 + KS > end || (ACROSS && width < W);
+    }
+
+    __device__ __forceinline__ i32x4 fix(int i, i32x4 v, uint32_t k0, uint32_t end) const
+    {
+        if (SHORT && (ACROSS ? width < EPC : end < EPC)) return v;  // (read piece by piece)
+        const uint32_t c = ACROSS ? column(i) : k0 + at[i], most = (ACROSS ? width : end) - EPC;
+        const uint32_t by = c > most ? c - most : 0;  // values to move by
+        if (by & (EPC / 2)) v = i32x4{v[2], v[3], 0, 0};
+        if (by & (EPC / 4)) v = i32x4{v[1], v[2], v[3], 0};
+        if (ES == 2 && (by & 1u)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (int)((uint32_t)v[e] >> 16 | (e < 3 ? (uint32_t)v[e + 1] << 16 : 0u));
+        }
+        const bool none = by >= EPC || (ACROSS && k0 + at[i] >= end);
+        return none ? i32x4{0, 0, 0, 0} : v;
     }
 
     __device__ __forceinline__ void put(uint8_t *lds, int i, i32x4 v) const
@@ -239,23 +276,32 @@ __device__ __forceinline__ TilePlace place_of(const TileParams &p, uint32_t BM, 
 // fragments of 32 x 32. B's columns are the instruction's rows, so that a lane
 // holds 4 neighbours of an output row (row l % 32, columns 8 a + 4 (l / 32) +
 // 0 .. 3 for a < 4). A step's operands are copied to LDS by loads that bypass
-// the registers, one step ahead, into the other of two buffers. One barrier
+// the registers, one step ahead into the other of two buffers, or three steps
+// ahead into four. One barrier
 // per step, before its last quarter is multiplied: by then every wave has
 // read all it needs of this step and its own copies of the next have landed.
 //
 // DIRECT needs both operands' rows to start on 16 bytes and to be whole
 // chunks of 16 along their rows; others come by way of registers.
-template <int DT, bool AX, bool BX, int OUT, int FM, int FN, bool DIRECT>
-__global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void linear_tile(TileParams p)
+template <int DT, bool AX, bool BX, int OUT, int FM, int FN, bool DIRECT, bool DEEP = false>
+__global__ __launch_bounds__(256, FM *FN == 16 || DEEP ? 1 : FM *FN == 4 ? 2 : 4) void linear_tile(TileParams p)
 {
     constexpr int BM = 64 * FM, BN = 64 * FN;
     typedef Operand<DT, AX, BM, FM, DIRECT> OpA;
     typedef Operand<DT, BX, BN, FN, DIRECT> OpB;
     constexpr bool IN_PLACE = FM * FN == 16;
+    constexpr uint32_t STAGES = DEEP ? 4 : 2;
+    constexpr bool FIVE = IN_PLACE && DIRECT;
+    static_assert(!DEEP || (DIRECT && FM * FN < 16), "");
+    constexpr int COPIES = OpA::COPIES + OpB::COPIES;
     constexpr uint32_t KS = OpA::KS;
     // an epilogue's slab of 32 rows of a wave has its place in one of them
     constexpr uint32_t SLAB_ROW = FN * 128 + 16;
-    __shared__ __attribute__((aligned(16))) uint8_t as0[OpA::BYTES], as1[OpA::BYTES], bs0[OpB::BYTES], bs1[OpB::BYTES];
+    // (an array for each step: the compiler then knows which of them a copy
+    // writes, and waits for no other)
+    constexpr uint32_t BYTES = FIVE ? OpA::BYTES : OpA::BYTES + OpB::BYTES;
+    __shared__ __attribute__((aligned(16))) uint8_t l0[BYTES], l1[BYTES], l2[FIVE || DEEP ? BYTES : 16],
+        l3[FIVE || DEEP ? BYTES : 16], l4[FIVE ? BYTES : 16];
     static_assert(FM == FN && 32 * SLAB_ROW <= OpA::BYTES, "");
     const uint32_t lane = threadIdx.x & 63u, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t wm = w >> 1, wn = w & 1u;
@@ -265,12 +311,30 @@ __global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void l
     const OpB B(p.b, p.b_stride, place.n0, p.n, wn);
 
     f32x16 acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int f = 0; f < FN; ++f) acc[i][f] = (f32x16)0.0f;
     i32x4 a[2][FM], b[2][FN];
-    [[maybe_unused]] i32x4 ra[OpA::COPIES], rb[OpB::COPIES];
+    // steps that are on their way in registers (not DIRECT)
+    constexpr int SETS = FM * FN == 16 ? 1 : 2;
+    [[maybe_unused]] i32x4 ra[SETS][OpA::COPIES], rb[SETS][OpB::COPIES];
+    [[maybe_unused]] const auto load = [&](int set, uint32_t s) {
+#pragma unroll
+        for (int i = 0; i < OpA::COPIES; ++i) ra[set][i] = A.load(i, s * KS, end);
+#pragma unroll
+        for (int i = 0; i < OpB::COPIES; ++i) rb[set][i] = B.load(i, s * KS, end);
+    };
+    [[maybe_unused]] const auto put = [&](int set, uint32_t s, uint8_t *as, uint8_t *bs) {
+        if (A.may_reach(s * KS, end)) {
+#pragma unroll
+            for (int i = 0; i < OpA::COPIES; ++i) ra[set][i] = A.fix(i, ra[set][i], s * KS, end);
+        }
+        if (B.may_reach(s * KS, end)) {
+#pragma unroll
+            for (int i = 0; i < OpB::COPIES; ++i) rb[set][i] = B.fix(i, rb[set][i], s * KS, end);
+        }
+#pragma unroll
+        for (int i = 0; i < OpA::COPIES; ++i) A.put(as, i, ra[set][i]);
+#pragma unroll
+        for (int i = 0; i < OpB::COPIES; ++i) B.put(bs, i, rb[set][i]);
+    };
 
     const auto read = [&](const uint8_t *as, const uint8_t *bs, int q, int into) {
 #pragma unroll
@@ -278,76 +342,163 @@ __global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void l
 #pragma unroll
         for (int f = 0; f < FN; ++f) b[into][f] = B.fragment(bs, q, f);
     };
-    // step s, whose operands are in (as, bs); the next one's go to (an, bn).
-    // Past the last step there are zeros.
-    const auto step = [&](uint32_t s, uint8_t *as, uint8_t *bs, uint8_t *an, uint8_t *bn) {
-        if constexpr (!DIRECT) {
-#pragma unroll
-            for (int i = 0; i < OpA::COPIES; ++i) ra[i] = A.load(i, (s + 1) * KS, end);
-#pragma unroll
-            for (int i = 0; i < OpB::COPIES; ++i) rb[i] = B.load(i, (s + 1) * KS, end);
-        }
+    // Step s, whose operands are in (as, bs) and the next one's in (an, bn); bb
+    // held B's of the step before. Past the last step there are zeros.
+    const auto step = [&](auto odd, uint32_t s, uint8_t *as, uint8_t *bs, uint8_t *an, uint8_t *bn, uint8_t *bb) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int cur = q & 1;
-            if (q < 3) {
-                read(as, bs, q + 1, cur ^ 1);
-            } else {
-                if constexpr (!DIRECT) {
-#pragma unroll
-                    for (int i = 0; i < OpA::COPIES; ++i) A.put(an, i, ra[i]);
-#pragma unroll
-                    for (int i = 0; i < OpB::COPIES; ++i) B.put(bn, i, rb[i]);
-                }
-                __builtin_amdgcn_s_waitcnt(0x0070);  // this wave's LDS accesses and copies are done
-                __syncthreads();
-                read(an, bn, 0, cur ^ 1);
+            const uint8_t *const ra_ = q < 3 ? as : an, *const rb_ = q < 3 ? bs : bn;
+            const int rq = q < 3 ? q + 1 : 0;
+            if (q == 3) {
+                // this wave's LDS reads and its copies of the next step are done
+                if constexpr (DIRECT)
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(FIVE ? OpA::COPIES : (STAGES - 2) * COPIES)
+                                 : "memory");
+                else  // (loads on their way are not waited for)
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            }
+            if constexpr (!IN_PLACE) read(ra_, rb_, rq, cur ^ 1);
+            if constexpr (!DIRECT) {
+                constexpr int next = (odd + 1) % SETS;
+                if (q == 1) put(next, s + 1, an, bn);
+                if (q == 2) load(next, s + 1 + SETS);
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
-                if constexpr (DIRECT) {
-                    if (q == 0) {
+                if constexpr (DIRECT && !FIVE) {
 #pragma unroll
-                        for (int i = 0; i < OpB::COPIES / FN; ++i) B.copy(bn, f * (OpB::COPIES / FN) + i, (s + 1) * KS, end);
-                    }
-                    if (q == 3) {
-#pragma unroll
-                        for (int i = 0; i < OpA::COPIES / FN; ++i) A.copy(as, f * (OpA::COPIES / FN) + i, (s + 2) * KS, end);
+                    for (int i = f * (OpA::COPIES / FN); i < (f + 1) * (OpA::COPIES / FN); ++i) {
+                        if (q == 0) B.copy(bb, i, (s - 1 + STAGES) * KS, end);
+                        if (q == 3) A.copy(as, i, (s + STAGES) * KS, end);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
-                    if constexpr (IN_PLACE) multiply_in_place<DT>(acc[i][f], b[cur][f], a[cur][i]);
-                    else acc[i][f] = multiply<DT>(b[cur][f], a[cur][i], acc[i][f]);
+                    if constexpr (IN_PLACE) {
+                        // the next quarter's fragments and the copies one by one between the products
+                        multiply_in_place<DT>(acc[i][f], b[cur][f], a[cur][i]);
+                        const int slot = f * 4 + i;
+                        if (slot == 2) b[cur ^ 1][0] = B.fragment(rb_, rq, 0);
+                        else if (slot == 0) a[cur ^ 1][0] = A.fragment(ra_, rq, 0);
+                        else if (slot < 10 && slot % 2 == 0) a[cur ^ 1][slot / 2 - 1] = A.fragment(ra_, rq, slot / 2 - 1);
+                        else if (slot % 2 == 0) b[cur ^ 1][slot / 2 - 4] = B.fragment(rb_, rq, slot / 2 - 4);
+                        if constexpr (FIVE) {
+                            if (i == 1) {
+                                if (q == 3) B.copy(as, f, (s + 2) * KS, end);
+                                if (q == 0) B.copy(bn, 4 + f, (s + 1) * KS, end);
+                                if (q == 1) A.copy(bb, f, (s + 2) * KS, end);
+                                if (q == 2) A.copy(bb, 4 + f, (s + 2) * KS, end);
+                            }
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    } else {
+                        acc[i][f] = multiply<DT>(b[cur][f], a[cur][i], acc[i][f]);
+                    }
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
+    // (while the first copies are on their way)
+    const auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                acc[i][f] = (f32x16)0.0f;
+                if constexpr (IN_PLACE) asm volatile("" : "+a"(acc[i][f]));  // (once, not on each way past the loops)
+            }
+    };
+    [[maybe_unused]] const auto copy_a = [&](uint8_t *as, uint32_t s) {
+#pragma unroll
+        for (int i = 0; i < OpA::COPIES; ++i) A.copy(as, i, s * KS, end);
+    };
+    [[maybe_unused]] const auto copy_b = [&](uint8_t *bs, uint32_t s) {
+#pragma unroll
+        for (int i = 0; i < OpB::COPIES; ++i) B.copy(bs, i, s * KS, end);
+    };
 
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
     uint32_t s = place.s0;
-    if constexpr (DIRECT) {
+    // (in the loops whole turns first: with a way out inside the turn the
+    // compiler waits for copies that just began, as on the ways out)
+    if constexpr (FIVE) {
+        copy_a(l0, s);
+        copy_b(l1, s);
+        copy_a(l2, s + 1);
 #pragma unroll
-        for (int i = 0; i < OpA::COPIES; ++i) A.copy(as0, i, s * KS, end);
-#pragma unroll
-        for (int i = 0; i < OpB::COPIES; ++i) B.copy(bs0, i, s * KS, end);
-#pragma unroll
-        for (int i = 0; i < OpA::COPIES; ++i) A.copy(as1, i, (s + 1) * KS, end);
+        for (int i = 0; i < 4; ++i) B.copy(l3, i, (s + 1) * KS, end);
+        clear();
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(OpA::COPIES + 4) : "memory");
+        read(l0, l1, 0, 0);
+        for (; s + 5 <= s1; s += 5) {
+            step(even, s, l0, l1, l2, l3, l4);
+            step(even, s + 1, l2, l3, l4, l0, l1);
+            step(even, s + 2, l4, l0, l1, l2, l3);
+            step(even, s + 3, l1, l2, l3, l4, l0);
+            step(even, s + 4, l3, l4, l0, l1, l2);
+        }
+        if (s < s1) {
+            step(even, s, l0, l1, l2, l3, l4);
+            if (s + 1 < s1) {
+                step(even, s + 1, l2, l3, l4, l0, l1);
+                if (s + 2 < s1) {
+                    step(even, s + 2, l4, l0, l1, l2, l3);
+                    if (s + 3 < s1) step(even, s + 3, l1, l2, l3, l4, l0);
+                }
+            }
+        }
+    } else if constexpr (DEEP) {
+        uint8_t *const b0 = l0 + OpA::BYTES, *const b1 = l1 + OpA::BYTES, *const b2 = l2 + OpA::BYTES,
+                *const b3 = l3 + OpA::BYTES;
+        copy_a(l0, s);
+        copy_b(b0, s);
+        copy_a(l1, s + 1);
+        copy_b(b1, s + 1);
+        copy_a(l2, s + 2);
+        copy_b(b2, s + 2);
+        copy_a(l3, s + 3);
+        clear();
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * COPIES + OpA::COPIES) : "memory");
+        read(l0, b0, 0, 0);
+        for (; s + 4 <= s1; s += 4) {
+            step(even, s, l0, b0, l1, b1, b3);
+            step(even, s + 1, l1, b1, l2, b2, b0);
+            step(even, s + 2, l2, b2, l3, b3, b1);
+            step(even, s + 3, l3, b3, l0, b0, b2);
+        }
+        if (s < s1) {
+            step(even, s, l0, b0, l1, b1, b3);
+            if (s + 1 < s1) {
+                step(even, s + 1, l1, b1, l2, b2, b0);
+                if (s + 2 < s1) step(even, s + 2, l2, b2, l3, b3, b1);
+            }
+        }
     } else {
+        uint8_t *const b0 = l0 + OpA::BYTES, *const b1 = l1 + OpA::BYTES;
+        if constexpr (DIRECT) {
+            copy_a(l0, s);
+            copy_b(b0, s);
+            copy_a(l1, s + 1);
+            clear();
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(OpA::COPIES) : "memory");
+        } else {
+            load(0, s);
+            clear();
+            put(0, s, l0, b0);
 #pragma unroll
-        for (int i = 0; i < OpA::COPIES; ++i) A.put(as0, i, A.load(i, s * KS, end));
-#pragma unroll
-        for (int i = 0; i < OpB::COPIES; ++i) B.put(bs0, i, B.load(i, s * KS, end));
+            for (uint32_t t = 1; t <= SETS; ++t) load(t % SETS, s + t);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        read(l0, b0, 0, 0);
+        for (; s + 2 <= s1; s += 2) {
+            step(even, s, l0, b0, l1, b1, b1);
+            step(odd, s + 1, l1, b1, l0, b0, b0);
+        }
+        if (s < s1) step(even, s, l0, b0, l1, b1, b1);
     }
-    __builtin_amdgcn_s_waitcnt(0x0070);
-    __syncthreads();
-    read(as0, bs0, 0, 0);
-    // two steps a turn, the second of an odd number on zeros
-    do {
-        step(s, as0, bs0, as1, bs1);
-        step(s + 1, as1, bs1, as0, bs0);
-        s += 2;
-    } while (s < s1);
     __builtin_amdgcn_s_waitcnt(0x0070);  // the copies past the end (zeros) are in LDS
     __syncthreads();                     // and every wave's last reads are done
 
@@ -360,10 +511,25 @@ __global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void l
     }
     // by way of LDS, so that 8 neighbours meet in a lane and rows are written
     // in long pieces
-    uint8_t *const slab = w == 0 ? as0 : w == 1 ? as1 : w == 2 ? bs0 : bs1;
-    const Mask mask = mask_of(p.part ? Drop{} : p.e.drop);
+    constexpr uint32_t HALF = FIVE ? 0 : OpA::BYTES;
+    uint8_t *const slab = FIVE ? (w == 0 ? l0 : w == 1 ? l1 : w == 2 ? l2 : l3) : (w & 1u ? l1 : l0) + (w >> 1) * HALF;
+    Epilogue e = p.e;
+    if (p.part) e = Epilogue{};  // the sums alone, of 32 bits
+    const Mask mask = mask_of(e.drop);
     constexpr uint32_t GROUPS = 4 * FN, ROWS = 64 / GROUPS;  // groups of 8 in a slab's row; rows at a time
-    const uint32_t r = lane & 31u, h = lane >> 5;
+    constexpr uint32_t TURNS = 32 / ROWS;
+    const uint32_t r = lane & 31u, h = lane >> 5, group = lane % GROUPS, slab_row = lane / GROUPS;
+    const uint32_t m_first = place.m0 + wm * FM * 32 + slab_row, n = place.n0 + wn * FN * 32 + group * 8;
+    float bias[8];
+    bias8<DT>(e, n, p.n, bias);  // (a lane's columns are the same in all rows)
+    // the residual is read four turns ahead
+    typename Elem<OUT>::vec8 ahead[4];
+    const auto look = [&](uint32_t turn) {
+        const uint32_t m = m_first + turn * ROWS;
+        return turn < FM * TURNS && m < p.m && n < p.n ? residual8<OUT>(e, m, n, p.n) : typename Elem<OUT>::vec8{};
+    };
+#pragma unroll
+    for (uint32_t t = 0; t < 4; ++t) ahead[t] = look(t);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -373,21 +539,28 @@ __global__ __launch_bounds__(256, FM *FN == 16 ? 1 : FM *FN == 4 ? 2 : 4) void l
                 *reinterpret_cast<f32x4 *>(slab + r * SLAB_ROW + (32 * f + 8 * q + 4 * h) * 4) =
                     f32x4{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (a wave's own: its LDS accesses stay in order)
+        const auto take = [&](uint32_t t, f32x4 *v) {
+            const uint8_t *const at = slab + (t * ROWS + slab_row) * SLAB_ROW + group * 32;
+            v[0] = *reinterpret_cast<const f32x4 *>(at);
+            v[1] = *reinterpret_cast<const f32x4 *>(at + 16);
+        };
+        f32x4 sums[2];
+        take(0, sums);
 #pragma unroll 1
-        for (uint32_t t = 0; t < 32 / ROWS; ++t) {
-            const uint32_t row = t * ROWS + lane / GROUPS, group = lane % GROUPS;
+        for (uint32_t t = i * TURNS; t < (i + 1) * TURNS; ++t) {
+            const auto residual = ahead[0];
+            ahead[0] = ahead[1];
+            ahead[1] = ahead[2];
+            ahead[2] = ahead[3];
+            ahead[3] = look(t + 4);
             float o[8];
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(slab + row * SLAB_ROW + group * 32);
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(slab + row * SLAB_ROW + group * 32 + 16);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                o[e] = lo[e];
-                o[4 + e] = hi[e];
-            }
-            const uint32_t m = place.m0 + (wm * FM + i) * 32 + row, n = place.n0 + wn * FN * 32 + group * 8;
+            for (int q = 0; q < 8; ++q) o[q] = sums[q >> 2][q & 3];
+            take(t + 1 < (i + 1) * TURNS ? t + 1 - i * TURNS : 0, sums);
+            const uint32_t m = m_first + t * ROWS;
             if (m < p.m && n < p.n) {
                 if (p.part) store8<kF32>(p.part + ((uint64_t)place.split * p.m + m) * p.n, n, p.n, o);
-                else finish8<DT, OUT>(p.e, mask, m, n, p.n, o);
+                else finish8<OUT>(e, mask, m, n, p.n, o, bias, residual);
             }
         }
         asm volatile("" ::: "memory");
@@ -409,7 +582,9 @@ __global__ __launch_bounds__(256) void join_parts(const float *__restrict__ part
 #pragma unroll
             for (int q = 0; q < 8; ++q) f[q] += v[q];
         }
-        finish8<DT, OUT>(e, mask, row, c, n, f);
+        float bias[8];
+        bias8<DT>(e, c, n, bias);
+        finish8<OUT>(e, mask, row, c, n, f, bias, residual8<OUT>(e, row, c, n));
     }
 }
 
@@ -419,7 +594,11 @@ struct Cut {
     uint32_t splits, steps_per_split;
 };
 
-Cut cut_of(uint64_t m, uint64_t n, uint64_t k, int dtype, bool direct)
+// How an operand's rows lie: whole chunks of 16 bytes, at any alignment, or
+// shorter than a chunk.
+enum Rows { kWhole = 0, kOdd = 1, kShort = 2 };
+
+Cut cut_of(uint64_t m, uint64_t n, uint64_t k, int dtype, Rows rows)
 {
     const uint32_t steps = (uint32_t)div_up(k * dtype_bytes(dtype), kStepBytes);
     struct Kind { int f; double step, ends; uint32_t per_cu; };
@@ -430,11 +609,17 @@ Cut cut_of(uint64_t m, uint64_t n, uint64_t k, int dtype, bool direct)
     double least = 0;
     for (int q = 0; q < 3; ++q) {
         const Kind &t = kinds[q];
-        if (t.f == 4 && (dtype == kF32 || !direct)) continue;
+        if ((t.f == 4 && dtype == kF32) || (t.f > 1 && rows == kShort)) continue;
+#ifdef SWEEP
+        if (getenv("CUT_F") && atoi(getenv("CUT_F")) != t.f) continue;
+#endif
         const uint64_t tiles = div_up(m, 64u * t.f) * div_up(n, 64u * t.f);
         for (uint32_t want = 1; want <= 16; want *= 2) {
             const uint32_t per = (uint32_t)div_up(steps, want), splits = (uint32_t)div_up(steps, per);
-            if (want > 1 && (per < 8 || splits != want)) continue;
+            if (want > 1 && (per < 4 || splits != want)) continue;
+#ifdef SWEEP
+        if (getenv("CUT_S") && atoi(getenv("CUT_S")) != (int)want) continue;
+#endif
             const uint64_t wgs = tiles * splits;
             if (wgs >= (1u << 24)) continue;  // a launch has fewer than 2^32 threads
             const uint64_t full = wgs / (256 * t.per_cu), rest = wgs % (256 * t.per_cu);
@@ -472,9 +657,12 @@ hipError_t launch_linear(const LinearArgs &g)
 {
     if (g.k == 0) return join<DT, OUT>(g, 0);
     constexpr uint64_t es = dtype_bytes(DT);
-    const bool direct = whole_chunks(g.a, g.a_stride * es, (AX ? g.m : g.k) * es) &&
-                        whole_chunks(g.b, g.b_stride * es, (BX ? g.n : g.k) * es);
-    const Cut c = cut_of(g.m, g.n, g.k, DT, direct);
+    const uint64_t a_row = (AX ? g.m : g.k) * es, b_row = (BX ? g.n : g.k) * es;
+    bool direct = whole_chunks(g.a, g.a_stride * es, a_row) && whole_chunks(g.b, g.b_stride * es, b_row);
+#ifdef SWEEP
+    direct = direct && !getenv("CUT_ODD");
+#endif
+    const Cut c = cut_of(g.m, g.n, g.k, DT, direct ? kWhole : a_row < 16 || b_row < 16 ? kShort : kOdd);
     TileParams p{};
     p.a = g.a;
     p.b = g.b;
@@ -490,12 +678,19 @@ hipError_t launch_linear(const LinearArgs &g)
     p.e = g.e;
     const uint32_t blocks = p.tiles_m * p.tiles_n * c.splits;
     if (direct) {
-        if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, true><<<blocks, 256, 0, g.stream>>>(p);
+        bool deep = blocks <= 256;
+#ifdef SWEEP
+        if (getenv("CUT_D")) deep = atoi(getenv("CUT_D"));
+#endif
+        if (c.f == 1 && deep) linear_tile<DT, AX, BX, OUT, 1, 1, true, true><<<blocks, 256, 0, g.stream>>>(p);
+        else if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, true><<<blocks, 256, 0, g.stream>>>(p);
+        else if (c.f == 2 && deep) linear_tile<DT, AX, BX, OUT, 2, 2, true, true><<<blocks, 256, 0, g.stream>>>(p);
         else if (c.f == 2) linear_tile<DT, AX, BX, OUT, 2, 2, true><<<blocks, 256, 0, g.stream>>>(p);
         else if constexpr (DT != kF32) linear_tile<DT, AX, BX, OUT, 4, 4, true><<<blocks, 256, 0, g.stream>>>(p);
     } else {
         if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, false><<<blocks, 256, 0, g.stream>>>(p);
-        else linear_tile<DT, AX, BX, OUT, 2, 2, false><<<blocks, 256, 0, g.stream>>>(p);
+        else if (c.f == 2) linear_tile<DT, AX, BX, OUT, 2, 2, false><<<blocks, 256, 0, g.stream>>>(p);
+        else if constexpr (DT != kF32) linear_tile<DT, AX, BX, OUT, 4, 4, false><<<blocks, 256, 0, g.stream>>>(p);
     }
     if (c.splits > 1) return join<DT, OUT>(g, c.splits);
     return hipGetLastError();
