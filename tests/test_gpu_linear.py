@@ -129,6 +129,19 @@ def test_a_value_that_is_not_finite_stays_in_its_row():
             assert torch.isnan(got[3]).all() and torch.isfinite(got[:3]).all() and torch.isfinite(got[4:]).all()
 
 
+@pytest.mark.parametrize("over", [1, 2, 5, 7])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_tile_of_less_than_a_chunk(over, dtype):
+    """Rows at odd places whose last tile has fewer columns than 16 bytes hold: of 64, 128 and 256 columns."""
+    for m, n, k in ((70, 64 + over, 128 + over), (1000, 2048 + over, 1024 + over), (2048 + over, 8192 + over, 200),
+                    (3000, 256 + over, 4096 + over)):
+        print(f"chunk m={m} n={n} k={k} {dtype}", flush=True)
+        x, w, _, dz, _ = layer(m, n, k, dtype)
+        ref.assert_near(cp.linear(x, w).y, *ref.linear(x, w, None, None, None, 0.0, None)[::2], "y")
+        ref.assert_near(cp.linear_dx(dz, w), *ref.product(dz, w, dtype), "dx")
+        ref.assert_near(cp.linear_dw(dz, x), *ref.product(dz.t(), x, torch.float32), "dw")
+
+
 def test_rows_that_overlap_and_odd_strides():
     for dtype in TYPES:
         x, w, bias, residual, _ = layer(90, 110, 300, dtype)

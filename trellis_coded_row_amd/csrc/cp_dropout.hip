@@ -5,6 +5,8 @@
 //   dz = drop(dy) act'(z), db = the sum of dz's rows
 //
 // Both read each value once and are bound by memory.
+#include <type_traits>
+
 #include "cp_linear_internal.h"
 
 namespace cpk {
@@ -15,15 +17,20 @@ namespace {
 // the rows. A wave takes 512 columns where there are as many.
 struct Layout {
     uint32_t tx, columns, groups;  // workgroups along the columns, and along the rows
+    bool runs;                     // their order, see place_of
 };
 
-constexpr uint32_t kRowsAtOnce = 4;  // rows a thread has in flight
+constexpr uint32_t kRowsAtOnce = 2;  // rows a thread has in flight
 
-Layout layout_of(uint64_t m, uint64_t n, uint64_t most)
+Layout layout_of(uint64_t m, uint64_t n, int dtype)
 {
+    constexpr uint64_t most = 2048;  // workgroups: eight for each compute unit
     Layout l{};
+    l.runs = n * dtype_bytes(dtype) % 128 != 0;
     l.tx = 0;
     while (l.tx < 6 && (8u << l.tx) < n) ++l.tx;
+    // (fewer lanes along a row where more than an eighth of them would lie past its end)
+    while (l.tx > 3 && div_up(n, 8u << l.tx) * (8u << l.tx) > n + n / 8 + 8) --l.tx;
     l.columns = (uint32_t)div_up(n, 8u << l.tx);
     const uint64_t at_once = (256u >> l.tx) * kRowsAtOnce, whole = div_up(m, at_once);
     const uint64_t want = div_up(most, l.columns);
@@ -32,131 +39,235 @@ Layout layout_of(uint64_t m, uint64_t n, uint64_t most)
     return l;
 }
 
+// 8 values of a row: all of them, or those before the row's end.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ typename Elem<DT>::vec8 get8(const typename Elem<DT>::raw *row, uint32_t c, uint32_t n)
+{
+    if constexpr (WHOLE) return *reinterpret_cast<const typename Elem<DT>::vec8 *>(row + c);
+    return load8<DT>(row, c, n);
+}
+
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void put8(typename Elem<DT>::raw *row, uint32_t c, uint32_t n, const float *f)
+{
+    store8<DT>(row, c, WHOLE ? c + 8 : n, f);
+}
+
+// A workgroup's place: its first column and row, and how far its rows lie apart.
+struct Place {
+    uint32_t group, column, groups, c, ty, row;
+};
+
+__device__ __forceinline__ Place place_of(uint32_t tx, uint32_t columns, bool runs)
+{
+    Place p;
+    // Places in turn, or for each of the 8 XCDs (workgroup ids taken in turn) a
+    // contiguous run of them, where rows start inside a line: the pieces of a
+    // row that share one then meet in one L2 (60,000 x 1,100 in f16: 66 -> 62
+    // us; rows that start on lines are read faster in turn, 8,192 x 16,384 in
+    // bf16 104 us against 108).
+    const uint32_t xcd = blockIdx.x & 7u, per = gridDim.x >> 3, extra = gridDim.x & 7u;
+    const uint32_t id = runs ? xcd * per + (xcd < extra ? xcd : extra) + (blockIdx.x >> 3) : blockIdx.x;
+    p.group = id / columns;
+    p.column = id - p.group * columns;
+    p.groups = gridDim.x / columns;
+    p.c = (p.column << (3 + tx)) + (threadIdx.x & ((1u << tx) - 1)) * 8;
+    p.ty = 256u >> tx;
+    p.row = threadIdx.x >> tx;
+    return p;
+}
+
+// Calls work(row) for this thread's rows, kRowsAtOnce at a time: first load(q,
+// row) for each, then work(q, row). Rows are counted in 64 bits: they end near
+// 2^31.
+template <typename Load, typename Work>
+__device__ __forceinline__ void over_rows(const Place &p, uint32_t rows, Load load, Work work)
+{
+    for (uint64_t at = (uint64_t)p.group * p.ty * kRowsAtOnce + p.row; at < rows;
+         at += (uint64_t)p.groups * p.ty * kRowsAtOnce) {
+#pragma unroll
+        for (uint32_t q = 0; q < kRowsAtOnce; ++q) load(q, at + q * p.ty < rows ? at + q * p.ty : at);
+#pragma unroll
+        for (uint32_t q = 0; q < kRowsAtOnce; ++q)
+            if (at + q * p.ty < rows) work(q, at + q * p.ty);
+    }
+}
+
 template <int DT, bool RESIDUAL>
 __global__ __launch_bounds__(256) void dropout_rows(const typename Elem<DT>::raw *x, uint64_t x_stride,
                                                     const typename Elem<DT>::raw *residual, uint64_t residual_stride,
-                                                    uint32_t n, uint32_t d, uint32_t tx, uint32_t columns, Drop drop,
+                                                    uint32_t n, uint32_t d, uint32_t tx, uint32_t columns, bool runs, Drop drop,
                                                     typename Elem<DT>::raw *y)
 {
     const Mask mask = mask_of(drop);
-    const uint32_t group = blockIdx.x / columns, column = blockIdx.x - group * columns, groups = gridDim.x / columns;
-    const uint32_t c = (column << (3 + tx)) + (threadIdx.x & ((1u << tx) - 1)) * 8, ty = 256u >> tx;
-    if (c >= d) return;
-    // (counted in 64 bits: the rows end near 2^31)
-    for (uint64_t at = (uint64_t)group * ty * kRowsAtOnce + (threadIdx.x >> tx); at < n;
-         at += (uint64_t)groups * ty * kRowsAtOnce) {
+    const Place p = place_of(tx, columns, runs);
+    const auto rows = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
         typename Elem<DT>::vec8 v[kRowsAtOnce], r[kRowsAtOnce];
+        over_rows(
+            p, n,
+            [&](uint32_t q, uint64_t row) {
+                v[q] = get8<DT, WHOLE>(x + row * x_stride, p.c, d);
+                if constexpr (RESIDUAL) r[q] = get8<DT, WHOLE>(residual + row * residual_stride, p.c, d);
+            },
+            [&](uint32_t q, uint64_t row) {
+                float f[8];
 #pragma unroll
-        for (uint32_t q = 0; q < kRowsAtOnce; ++q) {
-            const uint64_t row = at + q * ty < n ? at + q * ty : at;
-            v[q] = load8<DT>(x + row * x_stride, c, d);
-            if constexpr (RESIDUAL) r[q] = load8<DT>(residual + row * residual_stride, c, d);
-        }
+                for (int e = 0; e < 8; ++e) f[e] = Elem<DT>::get(v[q][e]);
+                if (mask.threshold) drop8(mask, (uint32_t)row, p.c, f);
+                if constexpr (RESIDUAL) {
 #pragma unroll
-        for (uint32_t q = 0; q < kRowsAtOnce; ++q) {
-            const uint64_t row = at + q * ty;
-            if (row >= n) break;
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = Elem<DT>::get(v[q][e]);
-            if (mask.threshold) drop8(mask, (uint32_t)row, c, f);
-            if constexpr (RESIDUAL) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] += Elem<DT>::get(r[q][e]);
+                    for (int e = 0; e < 8; ++e) f[e] += Elem<DT>::get(r[q][e]);
+                }
+                put8<DT, WHOLE>(y + row * d, p.c, d, f);
+            });
+    };
+    if (__all(p.c + 8 <= d)) rows(std::true_type{});
+    else if (p.c < d) rows(std::false_type{});
+}
+
+// The slope of an activation as cubics between 512 points from 0 up, 1 / kPoints
+// apart, in LDS: act'(-z) = 1 - act'(z) for the smooth ones, so that the odd
+// part act' - 1/2 is held for z >= 0. Hermite's cubics through the slope and its
+// derivative are off by 5e-9 (gelu), 3e-8 (silu) and 1e-8 (gelu_tanh) at most,
+// and past the last point the slope is 1 in 32 bits. A slope then takes ten
+// vector instructions and one read, where the formula takes up to 30 and
+// bounded the time: 8,192 x 16,384 in bf16 with gelu 258 us.
+template <int ACT>
+struct Slopes {
+    static constexpr float kPoints = ACT == kSilu ? 16.0f : 32.0f;
+    static constexpr bool TABLE = ACT == kGelu || ACT == kGeluTanh || ACT == kSilu;
+    static constexpr uint32_t COUNT = TABLE ? 512 : 1;
+
+    // the slope's derivative
+    static __device__ __forceinline__ float derivative(float z)
+    {
+        if constexpr (ACT == kGelu) return 0.3989422804014327f * exp_of(-0.5f * z * z) * (2.0f - z * z);
+        const float u = ACT == kSilu ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);
+        const float w = ACT == kSilu ? 1.0f : 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+        const float bend = ACT == kSilu ? 0.0f : 1.5957691216057308f * 0.26829f * z;
+        const float g = reciprocal(1.0f + exp_of(-u));
+        return g * (1.0f - g) * (2.0f * w + z * ((1.0f - 2.0f * g) * w * w + bend));
+    }
+
+    static __device__ __forceinline__ void fill(f32x4 *cubic)
+    {
+        if constexpr (TABLE) {
+            for (uint32_t i = threadIdx.x; i < COUNT; i += 256) {
+                const float z0 = (float)i / kPoints, z1 = (float)(i + 1) / kPoints;
+                const float p0 = act_slope<ACT>(z0) - 0.5f, p1 = act_slope<ACT>(z1) - 0.5f;
+                const float m0 = derivative(z0) / kPoints, m1 = derivative(z1) / kPoints;
+                cubic[i] = f32x4{p0, m0, 3.0f * (p1 - p0) - 2.0f * m0 - m1, 2.0f * (p0 - p1) + m0 + m1};
             }
-            store8<DT>(y + row * d, c, d, f);
+            __syncthreads();
         }
     }
-}
+
+    static __device__ __forceinline__ float at(const f32x4 *cubic, float z)
+    {
+        if constexpr (!TABLE) return act_slope<ACT>(z);
+        // (a minimum that keeps NaN; it then falls to point 0 with a NaN on the way to the next)
+        const float u = __builtin_elementwise_minimum(kPoints * __builtin_fabsf(z), 511.99997f);
+        const f32x4 c = cubic[(uint32_t)u];
+        const float f = __builtin_amdgcn_fractf(u);
+        const float odd = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(c[3], f, c[2]), f, c[1]), f, c[0]);
+        return 0.5f + __builtin_copysignf(odd, z);
+    }
+};
 
 template <int DT, int ACT>
 __global__ __launch_bounds__(256) void act_grad_rows(const typename Elem<DT>::raw *dy, uint64_t dy_stride,
                                                      const typename Elem<DT>::raw *z, uint64_t z_stride, uint32_t m,
-                                                     uint32_t n, uint32_t tx, uint32_t columns, Drop drop,
+                                                     uint32_t n, uint32_t tx, uint32_t columns, bool runs, Drop drop,
                                                      typename Elem<DT>::raw *dz, float *__restrict__ partial)
 {
-    __shared__ float sums[256][9];
+    typedef Slopes<ACT> S;
+    __shared__ __attribute__((aligned(16))) union {
+        f32x4 cubic[S::COUNT];
+        float sums[256][9];
+    } lds;
     const Mask mask = mask_of(drop);
-    const uint32_t group = blockIdx.x / columns, column = blockIdx.x - group * columns, groups = gridDim.x / columns;
-    const uint32_t c = (column << (3 + tx)) + (threadIdx.x & ((1u << tx) - 1)) * 8, ty = 256u >> tx;
+    const Place p = place_of(tx, columns, runs);
+    S::fill(lds.cubic);
     float db[8] = {};
-    for (uint64_t at = (uint64_t)group * ty * kRowsAtOnce + (threadIdx.x >> tx); at < m && c < n;
-         at += (uint64_t)groups * ty * kRowsAtOnce) {
+    const auto rows = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
         typename Elem<DT>::vec8 v[kRowsAtOnce], s[kRowsAtOnce];
+        over_rows(
+            p, m,
+            [&](uint32_t q, uint64_t row) {
+                v[q] = get8<DT, WHOLE>(dy + row * dy_stride, p.c, n);
+                if constexpr (ACT != kNone) s[q] = get8<DT, WHOLE>(z + row * z_stride, p.c, n);
+            },
+            [&](uint32_t q, uint64_t row) {
+                float f[8];
 #pragma unroll
-        for (uint32_t q = 0; q < kRowsAtOnce; ++q) {
-            const uint64_t row = at + q * ty < m ? at + q * ty : at;
-            v[q] = load8<DT>(dy + row * dy_stride, c, n);
-            if constexpr (ACT != kNone) s[q] = load8<DT>(z + row * z_stride, c, n);
-        }
+                for (int e = 0; e < 8; ++e) {
+                    f[e] = Elem<DT>::get(v[q][e]);
+                    if constexpr (ACT != kNone) f[e] *= S::at(lds.cubic, Elem<DT>::get(s[q][e]));
+                }
+                if (mask.threshold) drop8(mask, (uint32_t)row, p.c, f);
 #pragma unroll
-        for (uint32_t q = 0; q < kRowsAtOnce; ++q) {
-            const uint64_t row = at + q * ty;
-            if (row >= m) break;
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[e] = Elem<DT>::get(v[q][e]);
-                if constexpr (ACT != kNone) f[e] *= act_slope<ACT>(Elem<DT>::get(s[q][e]));
-            }
-            if (mask.threshold) drop8(mask, (uint32_t)row, c, f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) db[e] += f[e];
-            store8<DT>(dz + row * n, c, n, f);
-        }
-    }
+                for (int e = 0; e < 8; ++e) db[e] += f[e];
+                put8<DT, WHOLE>(dz + row * n, p.c, n, f);
+            });
+    };
+    if (__all(p.c + 8 <= n)) rows(std::true_type{});
+    else if (p.c < n) rows(std::false_type{});
     if (!partial) return;
     // the workgroup's rows, in order
+    __syncthreads();  // (the cubics' place is taken)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[threadIdx.x][e] = db[e];
+    for (int e = 0; e < 8; ++e) lds.sums[threadIdx.x][e] = db[e];
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < (8u << tx); i += 256) {
         float t = 0.0f;
-        for (uint32_t q = 0; q < ty; ++q) t += sums[(q << tx) + (i >> 3)][i & 7u];
-        const uint32_t at = (column << (3 + tx)) + i;
-        if (at < n) partial[(uint64_t)group * n + at] = t;
+        for (uint32_t q = 0; q < p.ty; ++q) t += lds.sums[(q << tx) + (i >> 3)][i & 7u];
+        const uint32_t at = (p.column << (3 + tx)) + i;
+        if (at < n) partial[(uint64_t)p.group * n + at] = t;
     }
 }
 
-// db = the sum of the partial rows, in order: 32 columns a workgroup, 8 threads
-// for each.
-__global__ __launch_bounds__(256) void sum_rows(const float *__restrict__ partial, uint32_t count, uint32_t n,
-                                                float *__restrict__ db)
+// db = the sum of the partial rows, in a fixed order: 32 columns a workgroup, 32
+// threads for each.
+__global__ __launch_bounds__(1024) void sum_rows(const float *__restrict__ partial, uint32_t count, uint32_t n,
+                                                 float *__restrict__ db)
 {
-    __shared__ float sums[8][32];
+    __shared__ float sums[32][33];
     const uint32_t g = threadIdx.x >> 5;
     for (uint32_t first = blockIdx.x * 32; first < n; first += gridDim.x * 32) {
         const uint32_t c = first + (threadIdx.x & 31u);
         float t = 0.0f;
-        if (c < n)
-            for (uint32_t p = g; p < count; p += 8) t += partial[(uint64_t)p * n + c];
+        if (c < n) {
+#pragma unroll 8
+            for (uint32_t p = g; p < count; p += 32) t += partial[(uint64_t)p * n + c];
+        }
         sums[g][threadIdx.x & 31u] = t;
         __syncthreads();
         if (g == 0 && c < n) {
 #pragma unroll
-            for (int q = 1; q < 8; ++q) t += sums[q][threadIdx.x & 31u];
+            for (int q = 1; q < 32; ++q) t += sums[q][threadIdx.x & 31u];
             db[c] = t;
         }
         __syncthreads();
     }
 }
 
-constexpr uint64_t kMostWorkgroups = 2048;  // eight for each compute unit
 constexpr uint64_t kMostSums = 1u << 20;    // a launch has fewer than 2^32 threads, and columns stay below 2^32
 
 template <int DT>
 hipError_t launch_dropout(const DropoutArgs &a)
 {
     typedef const typename Elem<DT>::raw *in;
-    const Layout l = layout_of(a.n, a.d, kMostWorkgroups);
+    const Layout l = layout_of(a.n, a.d, DT);
     const uint32_t blocks = l.columns * l.groups;
     if (a.residual)
         dropout_rows<DT, true><<<blocks, 256, 0, a.stream>>>((in)a.x, a.x_stride, (in)a.residual, a.residual_stride,
-                                                             (uint32_t)a.n, (uint32_t)a.d, l.tx, l.columns, a.drop,
+                                                             (uint32_t)a.n, (uint32_t)a.d, l.tx, l.columns, l.runs, a.drop,
                                                              (typename Elem<DT>::raw *)a.y);
     else
         dropout_rows<DT, false><<<blocks, 256, 0, a.stream>>>((in)a.x, a.x_stride, nullptr, 0, (uint32_t)a.n,
-                                                              (uint32_t)a.d, l.tx, l.columns, a.drop,
+                                                              (uint32_t)a.d, l.tx, l.columns, l.runs, a.drop,
                                                               (typename Elem<DT>::raw *)a.y);
     return hipGetLastError();
 }
@@ -165,13 +276,13 @@ template <int DT, int ACT>
 hipError_t launch_act_grad(const ActGradArgs &a)
 {
     typedef const typename Elem<DT>::raw *in;
-    const Layout l = layout_of(a.m, a.n, kMostWorkgroups);
+    const Layout l = layout_of(a.m, a.n, DT);
     act_grad_rows<DT, ACT><<<l.columns * l.groups, 256, 0, a.stream>>>(
-        (in)a.dy, a.dy_stride, (in)a.z, a.z_stride, (uint32_t)a.m, (uint32_t)a.n, l.tx, l.columns, a.drop,
+        (in)a.dy, a.dy_stride, (in)a.z, a.z_stride, (uint32_t)a.m, (uint32_t)a.n, l.tx, l.columns, l.runs, a.drop,
         (typename Elem<DT>::raw *)a.dz, a.db ? (float *)a.workspace : nullptr);
     if (a.db) {
         const uint64_t wgs = div_up(a.n, 32);
-        sum_rows<<<(uint32_t)(wgs < kMostSums ? wgs : kMostSums), 256, 0, a.stream>>>(
+        sum_rows<<<(uint32_t)(wgs < kMostSums ? wgs : kMostSums), 1024, 0, a.stream>>>(
             (const float *)a.workspace, l.groups, (uint32_t)a.n, a.db);
     }
     return hipGetLastError();
@@ -193,7 +304,7 @@ hipError_t act_grad_of(const ActGradArgs &a)
 
 uint64_t act_grad_workspace_bytes(uint64_t m, uint64_t n)
 {
-    return 4ull * layout_of(m, n, kMostWorkgroups).groups * n;
+    return 4ull * layout_of(m, n, kF32).groups * n;
 }
 
 hipError_t act_grad(const ActGradArgs &a)

@@ -93,6 +93,11 @@ __device__ __forceinline__ Mask mask_of(const Drop &d)
     return m;
 }
 
+__device__ __forceinline__ uint32_t exclusive_or(uint64_t a, uint32_t b, uint32_t c)
+{
+    return __builtin_amdgcn_bitop3_b32((uint32_t)a, b, c, 0x96);
+}
+
 // Philox4x32-10: ten rounds of two 32 x 32-bit products, whose halves change
 // places, with a key that moves by a constant. 20 products of 64 bits for 8
 // values: with 16 bits for each value their time stays below that of the
@@ -103,9 +108,9 @@ __device__ __forceinline__ u32x4 philox(uint32_t c0, uint32_t c1, const Mask &m)
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c0 = exclusive_or(b >> 32, c1, k0);
         c1 = (uint32_t)b;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c2 = exclusive_or(a >> 32, c3, k1);
         c3 = (uint32_t)a;
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;

@@ -4,9 +4,6 @@
 #pragma once
 
 #include <type_traits>
-#ifdef SWEEP
-#include <stdlib.h>
-#endif
 
 #include "cp_linear_internal.h"
 
@@ -101,7 +98,7 @@ struct Operand {
     uint64_t stride;         // bytes between rows
     uint32_t from[COPIES];   // byte offset of this lane's chunk of each copy (its row, where not DIRECT; not of ACROSS then)
     uint32_t at[COPIES];     // its first value's place in K (ACROSS: its row's)
-    uint32_t width;          // ACROSS: the columns from the tile's first on
+    uint32_t rows, width;    // all rows (ACROSS: columns), and those from the tile's first on
     uint32_t read[4];        // where this lane reads its fragments
     uint32_t w;
 
@@ -112,13 +109,14 @@ struct Operand {
         return W >= 128 ? k & 3u : (k >> 1) & 1u;
     }
 
-    // `first`: the tile's first row or column of `rows`; `part`: which of the
+    // `first`: the tile's first row or column of `rows_`; `part`: which of the
     // two waves along this operand reads
-    __device__ __forceinline__ Operand(const void *p, uint64_t stride_, uint32_t first, uint32_t rows, uint32_t part)
+    __device__ __forceinline__ Operand(const void *p, uint64_t stride_, uint32_t first, uint32_t rows_, uint32_t part)
     {
         const uint32_t lane = threadIdx.x & 63u;
         w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         stride = stride_;
+        rows = rows_;
         width = rows - first;
         base = (const uint8_t *)p + (ACROSS ? (uint64_t)first * ES : (uint64_t)first * stride);
 #pragma unroll
@@ -162,20 +160,21 @@ struct Operand {
     // chunk, where not SHORT): a chunk that
     // reaches past the end of its row is read from the row's last 16 bytes
     // and moved into place by fix(), which has to be called where may_reach()
-    // says so. `end` is at least 1.
+    // says so. (ACROSS, those may begin before the tile's first column.) `end`
+    // is at least 1.
     __device__ __forceinline__ i32x4 load(int i, uint32_t k0, uint32_t end) const
     {
         if constexpr (ACROSS) {
             const uint32_t first = k0 < end ? k0 : end - 1, last = end - 1 - first;  // (rows past the end: the last one)
-            const uint32_t row = at[i] < last ? at[i] : last, c = column(i), most = width - EPC;
-            const uint8_t *const p = base + (uint64_t)first * stride;
-            const uint32_t o = (__umul24(row, (uint32_t)stride / ES) + ((!SHORT || width >= EPC) && c > most ? most : c)) * ES;
-            return SHORT && width < EPC ? piecewise(p + o, row == at[i] && k0 < end && c < width ? width - c : 0)
-                               : *reinterpret_cast<const unaligned_i32x4 *>(p + o);
+            const uint32_t row = at[i] < last ? at[i] : last;
+            const int c = (int)column(i), most = (int)width - (int)EPC;
+            const uint8_t *const p = base + (uint64_t)first * stride + (uint64_t)__umul24(row, (uint32_t)stride / ES) * ES;
+            return SHORT && rows < EPC ? piecewise(p + c * (int)ES, row == at[i] && k0 < end && c < (int)width ? width - c : 0)
+                                       : *reinterpret_cast<const unaligned_i32x4 *>(p + (int64_t)((c < most ? c : most) * (int)ES));
         } else {
             const uint32_t c = k0 + at[i], most = end - EPC;
             return SHORT && end < EPC ? piecewise(base + from[i] + c * ES, c < end ? end - c : 0)
-                             : *reinterpret_cast<const unaligned_i32x4 *>(base + (from[i] + (c < most ? c : most) * ES));
+                                      : *reinterpret_cast<const unaligned_i32x4 *>(base + (from[i] + (c < most ? c : most) * ES));
         }
     }
 
@@ -205,9 +204,9 @@ struct Operand {
 
     __device__ __forceinline__ i32x4 fix(int i, i32x4 v, uint32_t k0, uint32_t end) const
     {
-        if (SHORT && (ACROSS ? width < EPC : end < EPC)) return v;  // (read piece by piece)
-        const uint32_t c = ACROSS ? column(i) : k0 + at[i], most = (ACROSS ? width : end) - EPC;
-        const uint32_t by = c > most ? c - most : 0;  // values to move by
+        if (SHORT && (ACROSS ? rows < EPC : end < EPC)) return v;  // (read piece by piece)
+        const int c = ACROSS ? (int)column(i) : (int)(k0 + at[i]), most = (int)(ACROSS ? width : end) - (int)EPC;
+        const uint32_t by = c > most ? (uint32_t)(c - most) : 0;  // values to move by
         if (by & (EPC / 2)) v = i32x4{v[2], v[3], 0, 0};
         if (by & (EPC / 4)) v = i32x4{v[1], v[2], v[3], 0};
         if (ES == 2 && (by & 1u)) {
@@ -522,45 +521,61 @@ __global__ __launch_bounds__(256, FM *FN == 16 || DEEP ? 1 : FM *FN == 4 ? 2 : 4
     const uint32_t m_first = place.m0 + wm * FM * 32 + slab_row, n = place.n0 + wn * FN * 32 + group * 8;
     float bias[8];
     bias8<DT>(e, n, p.n, bias);  // (a lane's columns are the same in all rows)
-    // the residual is read four turns ahead
-    typename Elem<OUT>::vec8 ahead[4];
+    const auto take = [&](uint32_t t, float *o) {  // turn t of the slab
+        const uint8_t *const at = slab + (t * ROWS + slab_row) * SLAB_ROW + group * 32;
+        const f32x4 lo = *reinterpret_cast<const f32x4 *>(at), hi = *reinterpret_cast<const f32x4 *>(at + 16);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            o[q] = lo[q];
+            o[4 + q] = hi[q];
+        }
+    };
+    constexpr uint32_t AHEAD = TURNS < 4 ? TURNS : 4;  // turns that the residual is read ahead
+    typename Elem<OUT>::vec8 ahead[AHEAD];
     const auto look = [&](uint32_t turn) {
         const uint32_t m = m_first + turn * ROWS;
         return turn < FM * TURNS && m < p.m && n < p.n ? residual8<OUT>(e, m, n, p.n) : typename Elem<OUT>::vec8{};
     };
+    if (e.residual) {
 #pragma unroll
-    for (uint32_t t = 0; t < 4; ++t) ahead[t] = look(t);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-#pragma unroll
-        for (int f = 0; f < FN; ++f)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<f32x4 *>(slab + r * SLAB_ROW + (32 * f + 8 * q + 4 * h) * 4) =
-                    f32x4{acc[i][f][4 * q], acc[i][f][4 * q + 1], acc[i][f][4 * q + 2], acc[i][f][4 * q + 3]};
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (a wave's own: its LDS accesses stay in order)
-        const auto take = [&](uint32_t t, f32x4 *v) {
-            const uint8_t *const at = slab + (t * ROWS + slab_row) * SLAB_ROW + group * 32;
-            v[0] = *reinterpret_cast<const f32x4 *>(at);
-            v[1] = *reinterpret_cast<const f32x4 *>(at + 16);
-        };
-        f32x4 sums[2];
-        take(0, sums);
+        for (uint32_t t = 0; t < AHEAD; ++t) ahead[t] = look(t);
+    }
 #pragma unroll 1
-        for (uint32_t t = i * TURNS; t < (i + 1) * TURNS; ++t) {
-            const auto residual = ahead[0];
-            ahead[0] = ahead[1];
-            ahead[1] = ahead[2];
-            ahead[2] = ahead[3];
-            ahead[3] = look(t + 4);
-            float o[8];
+    for (uint32_t i = 0; i < FM; ++i) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) o[q] = sums[q >> 2][q & 3];
-            take(t + 1 < (i + 1) * TURNS ? t + 1 - i * TURNS : 0, sums);
-            const uint32_t m = m_first + t * ROWS;
-            if (m < p.m && n < p.n) {
-                if (p.part) store8<kF32>(p.part + ((uint64_t)place.split * p.m + m) * p.n, n, p.n, o);
-                else finish8<OUT>(e, mask, m, n, p.n, o, bias, residual);
+        for (int j = 0; j < FM; ++j) {
+            if ((int)i != j) continue;
+#pragma unroll
+            for (int f = 0; f < FN; ++f)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<f32x4 *>(slab + r * SLAB_ROW + (32 * f + 8 * q + 4 * h) * 4) =
+                        f32x4{acc[j][f][4 * q], acc[j][f][4 * q + 1], acc[j][f][4 * q + 2], acc[j][f][4 * q + 3]};
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (a wave's own: its LDS accesses stay in order)
+        if (!e.residual) {
+            // (apart: where loads are waited for, so are the stores before them)
+#pragma unroll 1
+            for (uint32_t t = 0; t < TURNS; ++t) {
+                float o[8];
+                take(t, o);
+                const uint32_t m = m_first + (i * TURNS + t) * ROWS;
+                if (m < p.m && n < p.n) {
+                    if (p.part) store8<kF32>(p.part + ((uint64_t)place.split * p.m + m) * p.n, n, p.n, o);
+                    else finish8<OUT>(e, mask, m, n, p.n, o, bias, typename Elem<OUT>::vec8{});
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (uint32_t t = 0; t < TURNS; t += AHEAD) {
+#pragma unroll
+                for (uint32_t u = 0; u < AHEAD; ++u) {
+                    float o[8];
+                    take(t + u, o);
+                    const uint32_t m = m_first + (i * TURNS + t + u) * ROWS;
+                    if (m < p.m && n < p.n) finish8<OUT>(e, mask, m, n, p.n, o, bias, ahead[u]);
+                    ahead[u] = look(i * TURNS + t + u + AHEAD);
+                }
             }
         }
         asm volatile("" ::: "memory");
@@ -600,32 +615,31 @@ enum Rows { kWhole = 0, kOdd = 1, kShort = 2 };
 
 Cut cut_of(uint64_t m, uint64_t n, uint64_t k, int dtype, Rows rows)
 {
+    // us: a step of a workgroup that has its compute unit to itself, and of each
+    // where there are more for a unit; launch, first loads and epilogue; each
+    // further workgroup of a unit
+    struct Kind { int f; double alone, each, ends, more; };
+    static const Kind narrow[] = {{1, 0.15, 0.20, 4.7, 0.6}, {2, 0.29, 0.51, 7.4, 2.8}, {4, 1.52, 1.52, 18.0, 20.0}};
+    static const Kind odd[] = {{1, 0.46, 0.38, 4.8, 0.8}, {2, 0.80, 0.75, 7.5, 4.0}, {4, 2.0, 1.85, 22.0, 18.0}};
+    static const Kind wide[] = {{1, 0.43, 0.58, 4.6, 1.0}, {2, 1.82, 2.12, 8.0, 3.6}};
+    const Kind *const kinds = dtype == kF32 ? wide : rows == kWhole ? narrow : odd;
     const uint32_t steps = (uint32_t)div_up(k * dtype_bytes(dtype), kStepBytes);
-    struct Kind { int f; double step, ends; uint32_t per_cu; };
-    static const Kind narrow[] = {{4, 2400, 6000, 1}, {2, 900, 4000, 2}, {1, 330, 3000, 4}};
-    static const Kind wide[] = {{4, 16400, 6000, 1}, {2, 4200, 4000, 2}, {1, 1100, 3000, 4}};
-    const Kind *const kinds = dtype == kF32 ? wide : narrow;
     Cut best{};
     double least = 0;
-    for (int q = 0; q < 3; ++q) {
+    for (int q = 0; q < (dtype == kF32 ? 2 : 3); ++q) {
         const Kind &t = kinds[q];
-        if ((t.f == 4 && dtype == kF32) || (t.f > 1 && rows == kShort)) continue;
-#ifdef SWEEP
-        if (getenv("CUT_F") && atoi(getenv("CUT_F")) != t.f) continue;
-#endif
+        if (t.f > 1 && rows == kShort) continue;
         const uint64_t tiles = div_up(m, 64u * t.f) * div_up(n, 64u * t.f);
         for (uint32_t want = 1; want <= 16; want *= 2) {
             const uint32_t per = (uint32_t)div_up(steps, want), splits = (uint32_t)div_up(steps, per);
             if (want > 1 && (per < 4 || splits != want)) continue;
-#ifdef SWEEP
-        if (getenv("CUT_S") && atoi(getenv("CUT_S")) != (int)want) continue;
-#endif
             const uint64_t wgs = tiles * splits;
             if (wgs >= (1u << 24)) continue;  // a launch has fewer than 2^32 threads
-            const uint64_t full = wgs / (256 * t.per_cu), rest = wgs % (256 * t.per_cu);
-            const double share = rest ? (double)div_up(rest, 256) : 0;
-            double cost = (full * t.per_cu + share) * per * t.step + (full + (rest ? 1 : 0)) * t.ends;
-            if (splits > 1) cost += 6000 + (double)m * n * 4 * (splits + 1) / 2000;
+            // workgroups of a compute unit: between the mean and the most
+            const double load = 0.5 * ((double)div_up(wgs, 256) + wgs / 256.0);
+            const double step = t.alone > load * t.each ? t.alone : load * t.each;
+            double cost = t.ends + per * step + (load > 1 ? t.more * (load - 1) : 0);
+            if (splits > 1) cost += 3.4 + 0.13e-6 * 4 * (double)m * n * (splits + 1);
             if (best.f == 0 || cost < least) {
                 least = cost;
                 best = Cut{t.f, splits, per};
@@ -658,10 +672,7 @@ hipError_t launch_linear(const LinearArgs &g)
     if (g.k == 0) return join<DT, OUT>(g, 0);
     constexpr uint64_t es = dtype_bytes(DT);
     const uint64_t a_row = (AX ? g.m : g.k) * es, b_row = (BX ? g.n : g.k) * es;
-    bool direct = whole_chunks(g.a, g.a_stride * es, a_row) && whole_chunks(g.b, g.b_stride * es, b_row);
-#ifdef SWEEP
-    direct = direct && !getenv("CUT_ODD");
-#endif
+    const bool direct = whole_chunks(g.a, g.a_stride * es, a_row) && whole_chunks(g.b, g.b_stride * es, b_row);
     const Cut c = cut_of(g.m, g.n, g.k, DT, direct ? kWhole : a_row < 16 || b_row < 16 ? kShort : kOdd);
     TileParams p{};
     p.a = g.a;
@@ -678,10 +689,7 @@ hipError_t launch_linear(const LinearArgs &g)
     p.e = g.e;
     const uint32_t blocks = p.tiles_m * p.tiles_n * c.splits;
     if (direct) {
-        bool deep = blocks <= 256;
-#ifdef SWEEP
-        if (getenv("CUT_D")) deep = atoi(getenv("CUT_D"));
-#endif
+        const bool deep = blocks <= 256;
         if (c.f == 1 && deep) linear_tile<DT, AX, BX, OUT, 1, 1, true, true><<<blocks, 256, 0, g.stream>>>(p);
         else if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, true><<<blocks, 256, 0, g.stream>>>(p);
         else if (c.f == 2 && deep) linear_tile<DT, AX, BX, OUT, 2, 2, true, true><<<blocks, 256, 0, g.stream>>>(p);
