@@ -34,19 +34,19 @@ __device__ __forceinline__ f32x4 multiply16(i32x4 w, i32x4 x, f32x4 c)
 constexpr int kRowWaves = 8, kBatch = 8;                // waves of a workgroup; 64-byte pieces of a row read together
 constexpr uint32_t kBatchBytes = kBatch * 64;
 
-// Few rows of x (16 MT at most): w is read once, straight into registers, and
-// bounds the time: 8 x 4,096 x 24,576 in bf16 takes 41 us, 4.9 TB/s (a copy:
-// 5.1), 16 rows of x 49 and 32 rows 69, as each of the 256 workgroups reads all
-// of x from L2 (the tiles take 77 for any of these; with 64 rows 79 against
-// 111 here). A workgroup has 16 columns of y; its waves take runs of
+// Few rows of x: w is read once, straight into registers, and bounds the time:
+// 8 x 4,096 x 24,576 in bf16 takes 41 us, 4.9 TB/s (a copy: 5.1), one row 37, 16
+// rows 49, as each of the 256 workgroups reads all of x from L2. (The tiles take
+// 51 for anything up to 64 rows. With a second fragment of x here 17 rows took
+// 55, 32 rows 69; with four, 64 rows 111.) A workgroup has 16 columns of y; its waves take runs of
 // batches of K (512 bytes of each row of w: a lane has row l % 16 and the
 // 16-byte chunks l / 16 + 4 j of it) and add their sums through LDS. The next
 // batch is read while one is multiplied: 16 KiB of w in flight for each wave.
-template <int DT, int MT>
+template <int DT>
 __global__ __launch_bounds__(kRowWaves * 64, 2) void linear_rows(RowsParams p)
 {
     constexpr uint32_t ES = dtype_bytes(DT), EPC = 16 / ES;
-    __shared__ float sums[kRowWaves][16 * MT][17];
+    __shared__ float sums[kRowWaves][16][17];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t r = lane & 15u, g = lane >> 4;
     const uint32_t split = blockIdx.x / p.tiles, n0 = (blockIdx.x - split * p.tiles) * 16;
@@ -57,13 +57,8 @@ __global__ __launch_bounds__(kRowWaves * 64, 2) void linear_rows(RowsParams p)
     const uint32_t whole = p.k * ES / kBatchBytes;  // batches that do not reach past k
     // (rows past the end: the last one)
     const uint8_t *const pw = (const uint8_t *)p.w + (uint64_t)(n0 + r < p.n ? n0 + r : p.n - 1) * p.w_stride + g * 16;
-    const uint8_t *px[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        px[t] = (const uint8_t *)p.x + (uint64_t)(t * 16 + r < p.m ? t * 16 + r : p.m - 1) * p.x_stride + g * 16;
-    f32x4 acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = (f32x4)0.0f;
+    const uint8_t *const px = (const uint8_t *)p.x + (uint64_t)(r < p.m ? r : p.m - 1) * p.x_stride + g * 16;
+    f32x4 acc = (f32x4)0.0f;
 
     const auto load = [&](const uint8_t *row, uint32_t batch, i32x4 *v) {
         const uint8_t *const at = row + (uint64_t)batch * kBatchBytes;
@@ -89,37 +84,31 @@ __global__ __launch_bounds__(kRowWaves * 64, 2) void linear_rows(RowsParams p)
         }
     };
     struct Batch {
-        i32x4 w[kBatch], x[MT][kBatch];
+        i32x4 w[kBatch], x[kBatch];
     };
     const auto turn = [&](uint32_t b, Batch &now, Batch &next) {
         if (b >= b1) return;
         if (b + 1 < b1) {
             load(pw, b + 1, next.w);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) load(px[t], b + 1, next.x[t]);
+            load(px, b + 1, next.x);
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) acc[t] = multiply16<DT>(now.w[j], now.x[t][j], acc[t]);
+        for (int j = 0; j < kBatch; ++j) acc = multiply16<DT>(now.w[j], now.x[j], acc);
     };
     Batch u, v;
     if (b0 < b1) {
         load(pw, b0, u.w);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) load(px[t], b0, u.x[t]);
+        load(px, b0, u.x);
     }
     for (uint32_t b = b0; b < b1; b += 2) {
         turn(b, u, v);
         turn(b + 1, v, u);
     }
-    // lane l of fragment t has row 16 t + l % 16, columns 4 (l / 16) + e
+    // lane l has row l % 16, columns 4 (l / 16) + e
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sums[wave][t * 16 + r][4 * g + e] = acc[t][e];
+    for (int e = 0; e < 4; ++e) sums[wave][r][4 * g + e] = acc[e];
     __syncthreads();
-    if (threadIdx.x >= 32 * MT) return;
+    if (threadIdx.x >= 32) return;
     const uint32_t row = threadIdx.x >> 1, c = (threadIdx.x & 1u) * 8;
     if (row >= p.m || n0 + c >= p.n) return;
     float f[8] = {};
@@ -135,7 +124,7 @@ __global__ __launch_bounds__(kRowWaves * 64, 2) void linear_rows(RowsParams p)
     }
 }
 
-constexpr uint64_t kFewRows = 32;
+constexpr uint64_t kFewRows = 16;  // a fragment of x
 
 // Splits of K and a wave's batches for few rows.
 Cut rows_cut(uint64_t n, uint64_t k, int dtype)
@@ -164,8 +153,7 @@ hipError_t launch_rows(const LinearArgs &g)
     p.part = c.splits > 1 ? (float *)g.workspace : nullptr;
     p.e = g.e;
     const uint32_t blocks = p.tiles * c.splits;
-    if (g.m <= 16) linear_rows<DT, 1><<<blocks, kRowWaves * 64, 0, g.stream>>>(p);
-    else linear_rows<DT, 2><<<blocks, kRowWaves * 64, 0, g.stream>>>(p);
+    linear_rows<DT><<<blocks, kRowWaves * 64, 0, g.stream>>>(p);
     if (c.splits > 1) return join<DT, DT>(g, c.splits);
     return hipGetLastError();
 }
