@@ -17,12 +17,17 @@ namespace {
 // the rows. A wave takes 512 columns where there are as many.
 struct Layout {
     uint32_t tx, columns, groups;  // workgroups along the columns, and along the rows
+    bool many;                     // several rows in flight
     bool runs;                     // their order, see place_of
 };
 
-constexpr uint32_t kRowsAtOnce = 2;  // rows a thread has in flight
+// Rows a thread has in flight where there are enough for eight workgroups on
+// each compute unit, else one: four for dropout (393,216 x 512 in bf16: 146 us,
+// with two 159; 1,000 x 2,050: 6.1, with two 4.1, with one 3.9), two for the
+// gradient, which needs the registers.
+constexpr uint32_t kDropRows = 4, kGradRows = 2;
 
-Layout layout_of(uint64_t m, uint64_t n, int dtype)
+Layout layout_of(uint64_t m, uint64_t n, int dtype, uint32_t rows)
 {
     constexpr uint64_t most = 2048;  // workgroups: eight for each compute unit
     Layout l{};
@@ -32,7 +37,8 @@ Layout layout_of(uint64_t m, uint64_t n, int dtype)
     // (fewer lanes along a row where more than an eighth of them would lie past its end)
     while (l.tx > 3 && div_up(n, 8u << l.tx) * (8u << l.tx) > n + n / 8 + 8) --l.tx;
     l.columns = (uint32_t)div_up(n, 8u << l.tx);
-    const uint64_t at_once = (256u >> l.tx) * kRowsAtOnce, whole = div_up(m, at_once);
+    l.many = l.columns * div_up(m, (256u >> l.tx) * rows) >= most;
+    const uint64_t at_once = (256u >> l.tx) * (l.many ? rows : 1), whole = div_up(m, at_once);
     const uint64_t want = div_up(most, l.columns);
     l.groups = (uint32_t)(whole < want ? whole : want);
     if (l.groups == 0) l.groups = 1;
@@ -77,23 +83,23 @@ __device__ __forceinline__ Place place_of(uint32_t tx, uint32_t columns, bool ru
     return p;
 }
 
-// Calls work(row) for this thread's rows, kRowsAtOnce at a time: first load(q,
+// Calls work(row) for this thread's rows, R at a time: first load(q,
 // row) for each, then work(q, row). Rows are counted in 64 bits: they end near
 // 2^31.
-template <typename Load, typename Work>
+template <uint32_t R, typename Load, typename Work>
 __device__ __forceinline__ void over_rows(const Place &p, uint32_t rows, Load load, Work work)
 {
-    for (uint64_t at = (uint64_t)p.group * p.ty * kRowsAtOnce + p.row; at < rows;
-         at += (uint64_t)p.groups * p.ty * kRowsAtOnce) {
+    for (uint64_t at = (uint64_t)p.group * p.ty * R + p.row; at < rows;
+         at += (uint64_t)p.groups * p.ty * R) {
 #pragma unroll
-        for (uint32_t q = 0; q < kRowsAtOnce; ++q) load(q, at + q * p.ty < rows ? at + q * p.ty : at);
+        for (uint32_t q = 0; q < R; ++q) load(q, at + q * p.ty < rows ? at + q * p.ty : at);
 #pragma unroll
-        for (uint32_t q = 0; q < kRowsAtOnce; ++q)
+        for (uint32_t q = 0; q < R; ++q)
             if (at + q * p.ty < rows) work(q, at + q * p.ty);
     }
 }
 
-template <int DT, bool RESIDUAL>
+template <int DT, bool RESIDUAL, uint32_t R>
 __global__ __launch_bounds__(256) void dropout_rows(const typename Elem<DT>::raw *x, uint64_t x_stride,
                                                     const typename Elem<DT>::raw *residual, uint64_t residual_stride,
                                                     uint32_t n, uint32_t d, uint32_t tx, uint32_t columns, bool runs, Drop drop,
@@ -103,8 +109,8 @@ __global__ __launch_bounds__(256) void dropout_rows(const typename Elem<DT>::raw
     const Place p = place_of(tx, columns, runs);
     const auto rows = [&](auto whole) {
         constexpr bool WHOLE = decltype(whole)::value;
-        typename Elem<DT>::vec8 v[kRowsAtOnce], r[kRowsAtOnce];
-        over_rows(
+        typename Elem<DT>::vec8 v[R], r[R];
+        over_rows<R>(
             p, n,
             [&](uint32_t q, uint64_t row) {
                 v[q] = get8<DT, WHOLE>(x + row * x_stride, p.c, d);
@@ -175,7 +181,7 @@ struct Slopes {
     }
 };
 
-template <int DT, int ACT>
+template <int DT, int ACT, uint32_t R>
 __global__ __launch_bounds__(256) void act_grad_rows(const typename Elem<DT>::raw *dy, uint64_t dy_stride,
                                                      const typename Elem<DT>::raw *z, uint64_t z_stride, uint32_t m,
                                                      uint32_t n, uint32_t tx, uint32_t columns, bool runs, Drop drop,
@@ -192,8 +198,8 @@ __global__ __launch_bounds__(256) void act_grad_rows(const typename Elem<DT>::ra
     float db[8] = {};
     const auto rows = [&](auto whole) {
         constexpr bool WHOLE = decltype(whole)::value;
-        typename Elem<DT>::vec8 v[kRowsAtOnce], s[kRowsAtOnce];
-        over_rows(
+        typename Elem<DT>::vec8 v[R], s[R];
+        over_rows<R>(
             p, m,
             [&](uint32_t q, uint64_t row) {
                 v[q] = get8<DT, WHOLE>(dy + row * dy_stride, p.c, n);
@@ -255,29 +261,29 @@ __global__ __launch_bounds__(1024) void sum_rows(const float *__restrict__ parti
 
 constexpr uint64_t kMostSums = 1u << 20;    // a launch has fewer than 2^32 threads, and columns stay below 2^32
 
-template <int DT>
-hipError_t launch_dropout(const DropoutArgs &a)
+template <int DT, bool RESIDUAL, uint32_t R>
+hipError_t launch_dropout(const DropoutArgs &a, const Layout &l)
 {
     typedef const typename Elem<DT>::raw *in;
-    const Layout l = layout_of(a.n, a.d, DT);
-    const uint32_t blocks = l.columns * l.groups;
-    if (a.residual)
-        dropout_rows<DT, true><<<blocks, 256, 0, a.stream>>>((in)a.x, a.x_stride, (in)a.residual, a.residual_stride,
-                                                             (uint32_t)a.n, (uint32_t)a.d, l.tx, l.columns, l.runs, a.drop,
-                                                             (typename Elem<DT>::raw *)a.y);
-    else
-        dropout_rows<DT, false><<<blocks, 256, 0, a.stream>>>((in)a.x, a.x_stride, nullptr, 0, (uint32_t)a.n,
-                                                              (uint32_t)a.d, l.tx, l.columns, l.runs, a.drop,
-                                                              (typename Elem<DT>::raw *)a.y);
+    dropout_rows<DT, RESIDUAL, R><<<l.columns * l.groups, 256, 0, a.stream>>>(
+        (in)a.x, a.x_stride, (in)a.residual, a.residual_stride, (uint32_t)a.n, (uint32_t)a.d, l.tx, l.columns, l.runs,
+        a.drop, (typename Elem<DT>::raw *)a.y);
     return hipGetLastError();
 }
 
-template <int DT, int ACT>
-hipError_t launch_act_grad(const ActGradArgs &a)
+template <int DT>
+hipError_t dropout_of(const DropoutArgs &a)
+{
+    const Layout l = layout_of(a.n, a.d, DT, kDropRows);
+    if (a.residual) return l.many ? launch_dropout<DT, true, kDropRows>(a, l) : launch_dropout<DT, true, 1>(a, l);
+    return l.many ? launch_dropout<DT, false, kDropRows>(a, l) : launch_dropout<DT, false, 1>(a, l);
+}
+
+template <int DT, int ACT, uint32_t R>
+hipError_t launch_act_grad(const ActGradArgs &a, const Layout &l)
 {
     typedef const typename Elem<DT>::raw *in;
-    const Layout l = layout_of(a.m, a.n, DT);
-    act_grad_rows<DT, ACT><<<l.columns * l.groups, 256, 0, a.stream>>>(
+    act_grad_rows<DT, ACT, R><<<l.columns * l.groups, 256, 0, a.stream>>>(
         (in)a.dy, a.dy_stride, (in)a.z, a.z_stride, (uint32_t)a.m, (uint32_t)a.n, l.tx, l.columns, l.runs, a.drop,
         (typename Elem<DT>::raw *)a.dz, a.db ? (float *)a.workspace : nullptr);
     if (a.db) {
@@ -288,15 +294,22 @@ hipError_t launch_act_grad(const ActGradArgs &a)
     return hipGetLastError();
 }
 
+template <int DT, int ACT>
+hipError_t act_grad_with(const ActGradArgs &a)
+{
+    const Layout l = layout_of(a.m, a.n, DT, kGradRows);
+    return l.many ? launch_act_grad<DT, ACT, kGradRows>(a, l) : launch_act_grad<DT, ACT, 1>(a, l);
+}
+
 template <int DT>
 hipError_t act_grad_of(const ActGradArgs &a)
 {
     switch (a.act) {
-    case kRelu: return launch_act_grad<DT, kRelu>(a);
-    case kGelu: return launch_act_grad<DT, kGelu>(a);
-    case kGeluTanh: return launch_act_grad<DT, kGeluTanh>(a);
-    case kSilu: return launch_act_grad<DT, kSilu>(a);
-    default: return launch_act_grad<DT, kNone>(a);
+    case kRelu: return act_grad_with<DT, kRelu>(a);
+    case kGelu: return act_grad_with<DT, kGelu>(a);
+    case kGeluTanh: return act_grad_with<DT, kGeluTanh>(a);
+    case kSilu: return act_grad_with<DT, kSilu>(a);
+    default: return act_grad_with<DT, kNone>(a);
     }
 }
 
@@ -304,7 +317,7 @@ hipError_t act_grad_of(const ActGradArgs &a)
 
 uint64_t act_grad_workspace_bytes(uint64_t m, uint64_t n)
 {
-    return 4ull * layout_of(m, n, kF32).groups * n;
+    return 4ull * layout_of(m, n, kF32, kGradRows).groups * n;
 }
 
 hipError_t act_grad(const ActGradArgs &a)
@@ -316,9 +329,9 @@ hipError_t act_grad(const ActGradArgs &a)
 
 hipError_t dropout(const DropoutArgs &a)
 {
-    if (a.dtype == kBF16) return launch_dropout<kBF16>(a);
-    if (a.dtype == kF16) return launch_dropout<kF16>(a);
-    return launch_dropout<kF32>(a);
+    if (a.dtype == kBF16) return dropout_of<kBF16>(a);
+    if (a.dtype == kF16) return dropout_of<kF16>(a);
+    return dropout_of<kF32>(a);
 }
 
 }  // namespace cpk
