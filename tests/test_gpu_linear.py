@@ -16,7 +16,7 @@ TYPES = [torch.float32, torch.bfloat16, torch.float16]
 SIZES = [(1, 1, 1), (1, 7, 13), (2, 64, 8), (1, 200, 4096), (5, 33, 700), (8, 128, 24576), (16, 70, 1032), (17, 65, 130),
          (40, 100, 72), (64, 64, 64), (65, 129, 200), (100, 1000, 40), (130, 72, 1000), (257, 300, 96), (300, 520, 4100),
          (1000, 258, 1030)]
-LARGE = [(2048, 8192, 192), (4000, 4104, 328), (1030, 1000, 5000)]
+LARGE = [(4, 1000, 6000), (3, 70, 20001), (4, 5000, 300), (2048, 8192, 192), (4000, 4104, 328), (1030, 1000, 5000)]
 
 
 @pytest.fixture(scope="module", autouse=True)

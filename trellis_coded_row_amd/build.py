@@ -11,6 +11,8 @@ import re
 import subprocess
 import sys
 import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -40,7 +42,7 @@ TORCH_DEPS = TORCH_SOURCES + [os.path.join(CSRC, "cp_torch.h"), os.path.join(ROO
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
-    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     # no packed fp32 math: keep float code on plain (scalar-lane) instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-parameter", "-Wundef",
@@ -62,18 +64,27 @@ def is_stale() -> bool:
 
 
 def _hipcc(sources: list[str], lib: str, verbose: bool, extra_flags: list[str] | None) -> str:
+    """One object a source, several at a time, and the library from them."""
     tmp = lib + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include"), *sources, "-o", tmp]
-    return _run(cmd, tmp, lib, verbose)
+    flags = [*HIPCC_FLAGS, *(extra_flags or []), "-I", os.path.join(ROOT, "include")]
+    with tempfile.TemporaryDirectory() as folder, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objects = [os.path.join(folder, os.path.basename(s) + ".o") for s in sources]
+        list(pool.map(lambda pair: _compile([hipcc(), *flags, "-c", pair[0], "-o", pair[1]], lib, verbose),
+                      zip(sources, objects)))
+        return _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objects, "-o", tmp], tmp, lib, verbose)
 
 
-def _run(cmd: list[str], tmp: str, lib: str, verbose: bool) -> str:
+def _compile(cmd: list[str], lib: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"{os.path.basename(cmd[0])} failed building {os.path.basename(lib)}")
+
+
+def _run(cmd: list[str], tmp: str, lib: str, verbose: bool) -> str:
+    _compile(cmd, lib, verbose)
     os.replace(tmp, lib)
     return lib
 

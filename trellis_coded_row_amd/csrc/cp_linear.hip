@@ -59,6 +59,17 @@ __global__ __launch_bounds__(kRowWaves * 64, 2) void linear_rows(RowsParams p)
     const uint8_t *const pw = (const uint8_t *)p.w + (uint64_t)(n0 + r < p.n ? n0 + r : p.n - 1) * p.w_stride + g * 16;
     const uint8_t *const px = (const uint8_t *)p.x + (uint64_t)(r < p.m ? r : p.m - 1) * p.x_stride + g * 16;
     f32x4 acc = (f32x4)0.0f;
+    // what the epilogue reads, by the threads that will write 8 values of y each
+    const uint32_t row = threadIdx.x >> 1, c = (threadIdx.x & 1u) * 8;
+    const bool writes = row < p.m && n0 + c < p.n;
+    float bias[8];
+    typename Elem<DT>::vec8 residual = {};
+    Mask mask{};
+    if (writes && !p.part) {
+        bias8<DT>(p.e, n0 + c, p.n, bias);
+        residual = residual8<DT>(p.e, row, n0 + c, p.n);
+        mask = mask_of(p.e.drop);
+    }
 
     const auto load = [&](const uint8_t *row, uint32_t batch, i32x4 *v) {
         const uint8_t *const at = row + (uint64_t)batch * kBatchBytes;
@@ -108,38 +119,144 @@ __global__ __launch_bounds__(kRowWaves * 64, 2) void linear_rows(RowsParams p)
 #pragma unroll
     for (int e = 0; e < 4; ++e) sums[wave][r][4 * g + e] = acc[e];
     __syncthreads();
-    if (threadIdx.x >= 32) return;
-    const uint32_t row = threadIdx.x >> 1, c = (threadIdx.x & 1u) * 8;
-    if (row >= p.m || n0 + c >= p.n) return;
+    if (!writes) return;
     float f[8] = {};
 #pragma unroll
     for (int q = 0; q < kRowWaves; ++q)
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] += sums[q][row][c + e];
     if (p.part) store8<kF32>(p.part + ((uint64_t)split * p.m + row) * p.n, n0 + c, p.n, f);
-    else {
-        float bias[8];
-        bias8<DT>(p.e, n0 + c, p.n, bias);
-        finish8<DT>(p.e, mask_of(p.e.drop), row, n0 + c, p.n, f, bias, residual8<DT>(p.e, row, n0 + c, p.n));
+    else finish8<DT>(p.e, mask, row, n0 + c, p.n, f, bias, residual);
+}
+
+// Up to four rows of x, where 16 columns a workgroup would leave compute units
+// idle: the 4 x 4 instruction, whose 16 blocks take 16 neighbouring chunks of
+// K. A workgroup has 8 columns; its waves go by the four columns and the quarter of
+// K that they take. 1 x 1,024 x 4,096 in bf16: 5.6 us, call
+// included (with 16 columns 7.2).
+template <int DT>
+__device__ __forceinline__ f32x4 multiply4(i32x4 w, i32x4 x, f32x4 c)
+{
+    if constexpr (DT == kF32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c = __builtin_amdgcn_mfma_f32_4x4x1f32(__int_as_float(w[e]), __int_as_float(x[e]), c, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const i32x2 a = {w[2 * e], w[2 * e + 1]}, b = {x[2 * e], x[2 * e + 1]};
+            if constexpr (DT == kBF16)
+                c = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(i16x4, a), __builtin_bit_cast(i16x4, b), c, 0, 0, 0);
+            else
+                c = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0, 0);
+        }
     }
+    return c;
+}
+
+constexpr int kFourBatch = 4;                         // pieces of 256 bytes of a row that are read together
+constexpr uint32_t kFourBatchBytes = kFourBatch * 256;
+
+template <int DT>
+__global__ __launch_bounds__(kRowWaves * 64, 2) void linear_four_rows(RowsParams p)
+{
+    constexpr uint32_t ES = dtype_bytes(DT), EPC = 16 / ES;
+    __shared__ float sums[kRowWaves][4][4];
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r = lane & 3u, g = lane >> 2, half = wave & 1u, slice = wave >> 1;
+    const uint32_t split = blockIdx.x / p.tiles, n0 = (blockIdx.x - split * p.tiles) * 8, column = n0 + half * 4 + r;
+    const uint32_t batches = (p.k * ES + kFourBatchBytes - 1) / kFourBatchBytes;
+    const uint32_t first = (split * (kRowWaves / 2) + slice) * p.batches_per_wave;
+    const uint32_t b0 = first < batches ? first : batches;
+    const uint32_t b1 = b0 + p.batches_per_wave < batches ? b0 + p.batches_per_wave : batches;
+    // (rows past the end: the last one)
+    const uint8_t *const pw = (const uint8_t *)p.w + (uint64_t)(column < p.n ? column : p.n - 1) * p.w_stride;
+    const uint8_t *const px = (const uint8_t *)p.x + (uint64_t)(r < p.m ? r : p.m - 1) * p.x_stride;
+    const bool writes = threadIdx.x < p.m;  // 8 values of a row of y
+    float bias[8];
+    typename Elem<DT>::vec8 residual = {};
+    Mask mask{};
+    if (writes && !p.part) {
+        bias8<DT>(p.e, n0, p.n, bias);
+        residual = residual8<DT>(p.e, threadIdx.x, n0, p.n);
+        mask = mask_of(p.e.drop);
+    }
+    const auto load = [&](const uint8_t *row, uint32_t batch, i32x4 *v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < kFourBatch; ++j) {
+            const uint32_t c = batch * (kFourBatchBytes / ES) + j * 16 * EPC + g * EPC;
+            const typename Elem<DT>::raw *const at = (const typename Elem<DT>::raw *)row + c;
+            v[j] = i32x4{0, 0, 0, 0};
+            if (c + EPC <= p.k) {
+                v[j] = *reinterpret_cast<const unaligned_i32x4 *>(at);
+            } else if (c < p.k) {
+                typename Elem<DT>::raw e[EPC] = {};
+#pragma unroll
+                for (uint32_t q = 0; q < EPC; ++q)
+                    if (c + q < p.k) e[q] = at[q];
+                __builtin_memcpy(&v[j], e, 16);
+            }
+        }
+    };
+    f32x4 acc = (f32x4)0.0f;
+    i32x4 w[2][kFourBatch], x[2][kFourBatch];
+    if (b0 < b1) {
+        load(pw, b0, w[0]);
+        load(px, b0, x[0]);
+    }
+    const auto turn = [&](uint32_t b, i32x4 *wn, i32x4 *xn, i32x4 *wl, i32x4 *xl) __attribute__((always_inline)) {
+        if (b >= b1) return;
+        if (b + 1 < b1) {
+            load(pw, b + 1, wl);
+            load(px, b + 1, xl);
+        }
+#pragma unroll
+        for (int j = 0; j < kFourBatch; ++j) acc = multiply4<DT>(wn[j], xn[j], acc);
+    };
+    for (uint32_t b = b0; b < b1; b += 2) {
+        turn(b, w[0], x[0], w[1], x[1]);
+        turn(b + 1, w[1], x[1], w[0], x[0]);
+    }
+    // lane l has row l % 4 of x, this wave's four columns, of block l / 4
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int over = 4; over < 64; over *= 2) acc[e] += __shfl_xor(acc[e], over, 64);
+        if (lane < 4) sums[wave][r][e] = acc[e];
+    }
+    __syncthreads();
+    if (!writes) return;
+    float f[8] = {};
+#pragma unroll
+    for (int q = 0; q < kRowWaves; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[(q & 1) * 4 + e] += sums[q][threadIdx.x][e];
+    if (p.part) store8<kF32>(p.part + ((uint64_t)split * p.m + threadIdx.x) * p.n, n0, p.n, f);
+    else finish8<DT>(p.e, mask, threadIdx.x, n0, p.n, f, bias, residual);
 }
 
 constexpr uint64_t kFewRows = 16;  // a fragment of x
 
+// Whether few rows go by four: 16 columns a workgroup would leave compute units idle.
+bool by_four(uint64_t m, uint64_t n) { return m <= 4 && n <= 16 * 255; }
+
 // Splits of K and a wave's batches for few rows.
-Cut rows_cut(uint64_t n, uint64_t k, int dtype)
+Cut rows_cut(uint64_t m, uint64_t n, uint64_t k, int dtype)
 {
-    const uint64_t batches = div_up(k * dtype_bytes(dtype), kBatchBytes), tiles = div_up(n, 16);
+    const bool four = by_four(m, n);
+    const uint64_t batches = div_up(k * dtype_bytes(dtype), four ? kFourBatchBytes : kBatchBytes);
+    const uint64_t tiles = div_up(n, four ? 8 : 16), waves = four ? kRowWaves / 2 : kRowWaves;
     uint64_t splits = 1;
-    while (tiles * splits < 128 && batches >= 2 * splits * kRowWaves * 2) splits *= 2;
-    const uint64_t per = div_up(batches, splits * kRowWaves);
-    return Cut{0, (uint32_t)div_up(batches, per * kRowWaves), (uint32_t)per};
+    while (tiles * splits < 128 && batches >= 2 * splits * waves * (four ? 4 : 2)) splits *= 2;
+    const uint64_t per = div_up(batches, splits * waves);
+    return Cut{0, (uint32_t)div_up(batches, per * waves), (uint32_t)per};
 }
 
 template <int DT>
 hipError_t launch_rows(const LinearArgs &g)
 {
-    const Cut c = rows_cut(g.n, g.k, DT);
+    const Cut c = rows_cut(g.m, g.n, g.k, DT);
+    const bool four = by_four(g.m, g.n);
     RowsParams p{};
     p.x = g.a;
     p.w = g.b;
@@ -148,12 +265,13 @@ hipError_t launch_rows(const LinearArgs &g)
     p.m = (uint32_t)g.m;
     p.n = (uint32_t)g.n;
     p.k = (uint32_t)g.k;
-    p.tiles = (uint32_t)div_up(g.n, 16);
+    p.tiles = (uint32_t)div_up(g.n, four ? 8 : 16);
     p.batches_per_wave = c.steps_per_split;
     p.part = c.splits > 1 ? (float *)g.workspace : nullptr;
     p.e = g.e;
     const uint32_t blocks = p.tiles * c.splits;
-    linear_rows<DT><<<blocks, kRowWaves * 64, 0, g.stream>>>(p);
+    if (four) linear_four_rows<DT><<<blocks, kRowWaves * 64, 0, g.stream>>>(p);
+    else linear_rows<DT><<<blocks, kRowWaves * 64, 0, g.stream>>>(p);
     if (c.splits > 1) return join<DT, DT>(g, c.splits);
     return hipGetLastError();
 }
@@ -162,7 +280,7 @@ hipError_t launch_rows(const LinearArgs &g)
 
 uint64_t linear_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int dtype)
 {
-    uint64_t most = m <= kFewRows ? workspace_of(rows_cut(n, k, dtype), m, n) : 0;
+    uint64_t most = m <= kFewRows ? workspace_of(rows_cut(m, n, k, dtype), m, n) : 0;
     for (Rows rows : {kWhole, kOdd, kShort}) {
         const uint64_t bytes = workspace_of(cut_of(m, n, k, dtype, rows), m, n);
         most = bytes > most ? bytes : most;
