@@ -175,6 +175,21 @@ def test_no_columns_no_rows():
         assert dz.shape == (0, 10) and (db == 0).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 40, 64), (9, 40, 64), (70, 130, 72), (300, 264, 33), (2048, 8192, 64)])
+@pytest.mark.parametrize("dtype,tiny,large", [(torch.float32, 2.0**-140, 2.0**100), (torch.bfloat16, 2.0**-130, 2.0**100),
+                                              (torch.float16, 2.0**-22, 2.0**9)])
+def test_values_below_the_smallest_normal_one(m, n, k, dtype, tiny, large):
+    """Their products with large ones are exact, few and small whole multiples of tiny times large."""
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    x = torch.randint(-3, 4, (m, k), device="cuda", generator=gen).double()
+    w = torch.randint(-2, 3, (n, k), device="cuda", generator=gen).double()
+    d = torch.randint(-1, 2, (m, n), device="cuda", generator=gen).double()
+    want = (x @ w.t() * tiny * large).float()
+    assert torch.equal(cp.linear((x * tiny).to(dtype), (w * large).to(dtype)).y, want.to(dtype))
+    assert torch.equal(cp.linear_dx((d * large).to(dtype), (w * tiny).to(dtype)), (d @ w * tiny * large).float().to(dtype))
+    assert torch.equal(cp.linear_dw((d * large).to(dtype), (x * tiny).to(dtype)), (d.t() @ x * tiny * large).float())
+
+
 def test_into_rows_of_a_wider_matrix():
     x, _, _, dz, _ = layer(50, 20, 72, torch.bfloat16)
     wide = torch.full((22, 80), 5.0, device="cuda")

@@ -78,6 +78,7 @@ def test_linear_workspaces():
 
 def test_outputs_that_overlap_are_refused():
     size = 100 * 200 * 2
+    assert linear(y=T) == E and linear(z=T) == E
     assert linear(y=P) == E and linear(y=Q + 64) == E and linear(y=R) == E and linear(z=V + size - 2) == E
     assert linear(z=P) == E and linear(z=S) == E and linear(res=V + 2) == E and linear(res=V, rs=201, ys=200) == E
     dx = lambda dz=P, w=Q, dres=None, out=V: cp.cp_linear_dx(dz, 200, w, 64, dres, 64, BF16, 100, 200, 64, out, 1 << 47, 1 << 40, None)
@@ -85,7 +86,7 @@ def test_outputs_that_overlap_are_refused():
     dw = lambda dz=P, x=Q, out=V, add=0: cp.cp_linear_dw(dz, 200, x, 64, BF16, 100, 200, 64, add, out, 64, 1 << 47, 1 << 40, None)
     assert dw(out=P) == E and dw(out=Q + 4) == E and dw(out=V + 2) == E and dw(add=2) == E
     drop = lambda x=P, r=None, y=V, rng=T, p=0.5, xs=64: cp.cp_dropout(x, xs, r, 64, BF16, 100, 64, p, rng, y, None)
-    assert drop(y=P + 2) == E and drop(y=P, xs=65) == E and drop(r=V + 4) == E
+    assert drop(y=T) == E and drop(y=P + 2) == E and drop(y=P, xs=65) == E and drop(r=V + 4) == E
     grad = lambda dy=P, z=Q, dz=V, db=R, ds=64: cp.cp_linear_act_grad(dy, ds, z, 64, BF16, 100, 64, 4, 0.0, None, dz, db, 1 << 47,
                                                                     1 << 40, None)
     assert grad(dz=P + 2) == E and grad(dz=P, ds=70) == E and grad(dz=Q + 2) == E and grad(db=P) == E and grad(db=V) == E

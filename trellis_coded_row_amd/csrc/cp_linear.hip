@@ -278,14 +278,19 @@ hipError_t launch_rows(const LinearArgs &g)
 
 }  // namespace
 
-uint64_t linear_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int dtype)
+uint64_t linear_tile_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int dtype)
 {
-    uint64_t most = m <= kFewRows ? workspace_of(rows_cut(m, n, k, dtype), m, n) : 0;
+    uint64_t most = 0;
     for (Rows rows : {kWhole, kOdd, kShort}) {
         const uint64_t bytes = workspace_of(cut_of(m, n, k, dtype, rows), m, n);
         most = bytes > most ? bytes : most;
     }
     return most;
+}
+
+uint64_t linear_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int dtype)
+{
+    return m <= kFewRows ? workspace_of(rows_cut(m, n, k, dtype), m, n) : linear_tile_workspace_bytes(m, n, k, dtype);
 }
 
 template <int DT>

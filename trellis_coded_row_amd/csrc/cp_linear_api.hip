@@ -98,8 +98,8 @@ cp_status cp_linear(const void *x, uint64_t x_stride, const void *w, uint64_t w_
             return CP_ERR_INVALID_ARGUMENT;
     }
     const Range out[2] = {range_of(y, m, n, y_stride, es), range_of(z_out, m, n, n, es)};
-    const Range in[3] = {range_of(x, k ? m : 0, k, x_stride, es), range_of(w, k ? n : 0, k, w_stride, es),
-                         range_of(bias, 1, n, n, es)};
+    const Range in[4] = {range_of(x, k ? m : 0, k, x_stride, es), range_of(w, k ? n : 0, k, w_stride, es),
+                         range_of(bias, 1, n, n, es), range_of(a.e.drop.rng, 1, 2, 2, 8)};
     for (const Range &i : in)
         if (overlap(out[0], i) || overlap(out[1], i)) return CP_ERR_INVALID_ARGUMENT;
     const Range r = range_of(residual, m, n, residual_stride, es);
@@ -149,12 +149,13 @@ cp_status cp_linear_act_grad(const void *dy, uint64_t dy_stride, const void *z, 
         if (db && !workspace_ok(workspace, workspace_bytes, cpk::act_grad_workspace_bytes(m, n)))
             return CP_ERR_INVALID_ARGUMENT;
         const Range out = range_of(dz, m, n, n, es), sums = range_of(db, 1, n, n, 4);
+        const Range numbers = range_of(a.drop.rng, 1, 2, 2, 8);
         const Range in[2] = {range_of(dy, m, n, dy_stride, es),
                              range_of(act == CP_ACT_NONE ? nullptr : z, m, n, z_stride, es)};
         const bool itself[2] = {dy == dz && (m == 1 || dy_stride == n), z == dz && (m == 1 || z_stride == n)};
         for (int q = 0; q < 2; ++q)
             if (overlap(sums, in[q]) || (!itself[q] && overlap(out, in[q]))) return CP_ERR_INVALID_ARGUMENT;
-        if (overlap(out, sums)) return CP_ERR_INVALID_ARGUMENT;
+        if (overlap(out, sums) || overlap(out, numbers) || overlap(sums, numbers)) return CP_ERR_INVALID_ARGUMENT;
     }
     if (m == 0 && !db) return CP_OK;
     forget_earlier_error();
@@ -177,7 +178,7 @@ cp_status cp_linear_act_grad(const void *dy, uint64_t dy_stride, const void *z, 
 uint64_t cp_linear_dx_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, cp_dtype dtype)
 {
     if (!dtype_ok(dtype) || m == 0 || n == 0 || k == 0 || n > kMaxStride || k > kMaxStride || too_large(m, k)) return 0;
-    return cpk::linear_workspace_bytes(m, k, n, dtype);
+    return cpk::linear_tile_workspace_bytes(m, k, n, dtype);
 }
 
 cp_status cp_linear_dx(const void *dz, uint64_t dz_stride, const void *w, uint64_t w_stride, const void *dres,
@@ -194,7 +195,7 @@ cp_status cp_linear_dx(const void *dz, uint64_t dz_stride, const void *w, uint64
     if (!good(dx, es)) return CP_ERR_INVALID_ARGUMENT;
     if (n > 0) {
         if (!good(dz, es) || !good(w, es)) return CP_ERR_INVALID_ARGUMENT;
-        if (!workspace_ok(workspace, workspace_bytes, cpk::linear_workspace_bytes(m, k, n, dtype)))
+        if (!workspace_ok(workspace, workspace_bytes, cpk::linear_tile_workspace_bytes(m, k, n, dtype)))
             return CP_ERR_INVALID_ARGUMENT;
     }
     const Range out = range_of(dx, m, k, k, es);
@@ -226,7 +227,7 @@ uint64_t cp_linear_dw_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, cp_dty
     if (!dtype_ok(dtype) || m == 0 || n == 0 || k == 0 || m > kMaxRows || n > kMaxStride || k > kMaxStride ||
         too_large(n, k))
         return 0;
-    return cpk::linear_workspace_bytes(n, k, m, dtype);
+    return cpk::linear_tile_workspace_bytes(n, k, m, dtype);
 }
 
 cp_status cp_linear_dw(const void *dz, uint64_t dz_stride, const void *x, uint64_t x_stride, cp_dtype dtype,
@@ -243,7 +244,7 @@ cp_status cp_linear_dw(const void *dz, uint64_t dz_stride, const void *x, uint64
     if (!good(dw, 4)) return CP_ERR_INVALID_ARGUMENT;
     if (m > 0) {
         if (!good(dz, es) || !good(x, es)) return CP_ERR_INVALID_ARGUMENT;
-        if (!workspace_ok(workspace, workspace_bytes, cpk::linear_workspace_bytes(n, k, m, dtype)))
+        if (!workspace_ok(workspace, workspace_bytes, cpk::linear_tile_workspace_bytes(n, k, m, dtype)))
             return CP_ERR_INVALID_ARGUMENT;
     }
     const Range out = range_of(dw, n, k, dw_stride, 4);
@@ -285,6 +286,7 @@ cp_status cp_dropout(const void *x, uint64_t x_stride, const void *residual, uin
     if (!(residual == y && (n == 1 || residual_stride == d)) &&
         overlap(out, range_of(residual, n, d, residual_stride, es)))
         return CP_ERR_INVALID_ARGUMENT;
+    if (overlap(out, range_of(a.drop.rng, 1, 2, 2, 8))) return CP_ERR_INVALID_ARGUMENT;
     forget_earlier_error();
     a.x = x;
     a.residual = residual;

@@ -39,7 +39,9 @@ struct LinearArgs {
     uint8_t *workspace;
     hipStream_t stream;
 };
+// (cp_linear's; and of the other two, with their outputs' m and n and their sums' k)
 uint64_t linear_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int dtype);
+uint64_t linear_tile_workspace_bytes(uint64_t m, uint64_t n, uint64_t k, int dtype);
 hipError_t linear_rows_by_rows(const LinearArgs &a);      // A, B: rows of K (cp_linear)
 hipError_t linear_rows_by_columns(const LinearArgs &a);   // B across (cp_linear_dx)
 hipError_t linear_columns_by_columns(const LinearArgs &a);  // both across, 32-bit output (cp_linear_dw)
