@@ -35,7 +35,7 @@ constexpr int kRowWaves = 8, kBatch = 8;                // waves of a workgroup;
 constexpr uint32_t kBatchBytes = kBatch * 64;
 
 // Few rows of x: w is read once, straight into registers, and bounds the time:
-// 8 x 4,096 x 24,576 in bf16 takes 41 us, 4.9 TB/s (a copy: 5.1), one row 37, 16
+// 8 x 4,096 x 24,576 in bf16 takes 40.5 us, 5.0 TB/s (a copy: 5.1), one row 37, 16
 // rows 49, as each of the 256 workgroups reads all of x from L2. (The tiles take
 // 51 for anything up to 64 rows. With a second fragment of x here 17 rows took
 // 55, 32 rows 69; with four, 64 rows 111.) A workgroup has 16 columns of y; its waves take runs of

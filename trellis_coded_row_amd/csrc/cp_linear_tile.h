@@ -277,10 +277,21 @@ __device__ __forceinline__ TilePlace place_of(const TileParams &p, uint32_t BM, 
 // fragments of 32 x 32. B's columns are the instruction's rows, so that a lane
 // holds 4 neighbours of an output row (row l % 32, columns 8 a + 4 (l / 32) +
 // 0 .. 3 for a < 4). A step's operands are copied to LDS by loads that bypass
-// the registers, one step ahead into the other of two buffers, or three steps
-// ahead into four. One barrier
-// per step, before its last quarter is multiplied: by then every wave has
-// read all it needs of this step and its own copies of the next have landed.
+// the registers: one step ahead into the other of two buffers, three steps
+// ahead into four (DEEP), or, with 4 x 4 fragments, one to two steps ahead into
+// five places of one operand's step each. One barrier per step, before its
+// last quarter is multiplied: by then every wave has read all it needs of this
+// step and its own copies of the next have landed.
+//
+// A step of 4 x 4 fragments reads 8 of them for 16 products, which LDS hides
+// behind the products; its accumulators leave one wave for each SIMD, so the
+// next fragments are read between the products of the present ones. 4,096 x
+// 4,096 x 24,576 in bf16: cp_linear 571 to 605 us (1.36 to 1.44 PFLOP/s; the
+// vendor library's product 542 to 628), cp_linear_dx 640 to 652 (618 to 722),
+// cp_linear_dw 665 to 677 (709 to 824 for a 16-bit output). Its matrix units
+// are busy 83% of the cycles (71 and 68% where operands are read across, at two LDS
+// reads a fragment), at a clock that gives way to the power they draw: with
+// zeros for operands the same launches take 458, 498 and 495 us.
 //
 // DIRECT needs both operands' rows to start on 16 bytes and to be whole
 // chunks of 16 along their rows; others come by way of registers.
@@ -617,9 +628,14 @@ enum Rows { kWhole = 0, kOdd = 1, kShort = 2 };
 
 Cut cut_of(uint64_t m, uint64_t n, uint64_t k, int dtype, Rows rows)
 {
-    // us: a step of a workgroup that has its compute unit to itself, and of each
-    // where there are more for a unit; launch, first loads and epilogue; each
-    // further workgroup of a unit
+    // us, fitted to measured times of every form: a step of a workgroup that has
+    // its compute unit to itself, and of each where there are more for a unit;
+    // launch, first loads and epilogue; each further workgroup of a unit. Large
+    // tiles read less, small ones and splits fill the chip: 4,096 x 4,096 x
+    // 24,576 takes 571 us with f = 4 and 779 with 2, 2,000^3 takes 35, 26 and 46
+    // with 1, 2 and 4, 256 x 1,024 x 1,024 takes 6.5, 11 and 28; 64 x 4,096 x
+    // 24,576 with f = 1 takes 121, 72, 53 and 50 in 1, 2, 4 and 8 splits, 8,192 x
+    // 1,024 x 512 with f = 2 takes 15 whole and 41 in 2.
     struct Kind { int f; double alone, each, ends, more; };
     static const Kind narrow[] = {{1, 0.15, 0.20, 4.7, 0.6}, {2, 0.29, 0.51, 7.4, 2.8}, {4, 1.52, 1.52, 18.0, 20.0}};
     static const Kind odd[] = {{1, 0.46, 0.38, 4.8, 0.8}, {2, 0.80, 0.75, 7.5, 4.0}, {4, 2.0, 1.85, 22.0, 18.0}};
@@ -691,6 +707,10 @@ hipError_t launch_linear(const LinearArgs &g)
     p.e = g.e;
     const uint32_t blocks = p.tiles_m * p.tiles_n * c.splits;
     if (direct) {
+        // four steps' buffers where no compute unit has two workgroups: 64 x 4,096
+        // x 24,576 in 4 splits 53 us, with two 82; 2,000^3 26 and 31. Where one
+        // has, the other hides the copies, and twice the LDS keeps it out: 8,192 x
+        // 1,024 x 512 takes 19 us with four and 15 with two.
         const bool deep = blocks <= 256;
         if (c.f == 1 && deep) linear_tile<DT, AX, BX, OUT, 1, 1, true, true><<<blocks, 256, 0, g.stream>>>(p);
         else if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, true><<<blocks, 256, 0, g.stream>>>(p);
