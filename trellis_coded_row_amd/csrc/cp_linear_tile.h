@@ -87,9 +87,9 @@ __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15");
 //
 // The copy to LDS writes lane after lane, so the exchange is made in the
 // address that a lane loads from.
-template <int DT, bool ACROSS, int W, int F, bool DIRECT>
+// SHORT: rows of less than a chunk are read too.
+template <int DT, bool ACROSS, int W, int F, bool DIRECT, bool SHORT>
 struct Operand {
-    static constexpr bool SHORT = F == 1;  // rows of less than a chunk are read too
     static constexpr uint32_t ES = dtype_bytes(DT), EPC = 16 / ES;  // values of a 16-byte chunk
     static constexpr uint32_t KS = kStepBytes / ES;                 // values of K in a step
     static constexpr uint32_t RB = W * ES;                          // bytes of a row in LDS (ACROSS)
@@ -295,12 +295,12 @@ __device__ __forceinline__ TilePlace place_of(const TileParams &p, uint32_t BM, 
 //
 // DIRECT needs both operands' rows to start on 16 bytes and to be whole
 // chunks of 16 along their rows; others come by way of registers.
-template <int DT, bool AX, bool BX, int OUT, int FM, int FN, bool DIRECT, bool DEEP = false>
+template <int DT, bool AX, bool BX, int OUT, int FM, int FN, bool DIRECT, bool DEEP = false, bool SHORT = false>
 __global__ __launch_bounds__(256, FM *FN == 16 || DEEP ? 1 : FM *FN == 4 ? 2 : 4) void linear_tile(TileParams p)
 {
     constexpr int BM = 64 * FM, BN = 64 * FN;
-    typedef Operand<DT, AX, BM, FM, DIRECT> OpA;
-    typedef Operand<DT, BX, BN, FN, DIRECT> OpB;
+    typedef Operand<DT, AX, BM, FM, DIRECT, SHORT> OpA;
+    typedef Operand<DT, BX, BN, FN, DIRECT, SHORT> OpB;
     constexpr bool IN_PLACE = FM * FN == 16;
     constexpr uint32_t STAGES = DEEP ? 4 : 2;
     constexpr bool FIVE = IN_PLACE && DIRECT;
@@ -325,6 +325,8 @@ __global__ __launch_bounds__(256, FM *FN == 16 || DEEP ? 1 : FM *FN == 4 ? 2 : 4
     f32x16 acc[FM][FN];
     i32x4 a[2][FM], b[2][FN];
     // steps that are on their way in registers (not DIRECT)
+    // (with four of them cp_linear_dx took 25.4 us against 24.9 for 1,000 x 1,030 from 2,050 in f16, 183 against
+    // 158 for 2,001^3 in f32)
     constexpr int SETS = FM * FN == 16 ? 1 : 2;
     [[maybe_unused]] i32x4 ra[SETS][OpA::COPIES], rb[SETS][OpB::COPIES];
     [[maybe_unused]] const auto load = [&](int set, uint32_t s) {
@@ -691,7 +693,8 @@ hipError_t launch_linear(const LinearArgs &g)
     constexpr uint64_t es = dtype_bytes(DT);
     const uint64_t a_row = (AX ? g.m : g.k) * es, b_row = (BX ? g.n : g.k) * es;
     const bool direct = whole_chunks(g.a, g.a_stride * es, a_row) && whole_chunks(g.b, g.b_stride * es, b_row);
-    const Cut c = cut_of(g.m, g.n, g.k, DT, direct ? kWhole : a_row < 16 || b_row < 16 ? kShort : kOdd);
+    const Rows rows = direct ? kWhole : a_row < 16 || b_row < 16 ? kShort : kOdd;
+    const Cut c = cut_of(g.m, g.n, g.k, DT, rows);
     TileParams p{};
     p.a = g.a;
     p.b = g.b;
@@ -718,7 +721,10 @@ hipError_t launch_linear(const LinearArgs &g)
         else if (c.f == 2) linear_tile<DT, AX, BX, OUT, 2, 2, true><<<blocks, 256, 0, g.stream>>>(p);
         else if constexpr (DT != kF32) linear_tile<DT, AX, BX, OUT, 4, 4, true><<<blocks, 256, 0, g.stream>>>(p);
     } else {
-        if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, false><<<blocks, 256, 0, g.stream>>>(p);
+        // (a form of its own: with a way around each load the compiler waits for later loads too. 1,000 x
+        // 1,030 from 2,050 in f16 25 us against 28, 33 x 8,001 from 1,001 11 against 14)
+        if (rows == kShort) linear_tile<DT, AX, BX, OUT, 1, 1, false, false, true><<<blocks, 256, 0, g.stream>>>(p);
+        else if (c.f == 1) linear_tile<DT, AX, BX, OUT, 1, 1, false><<<blocks, 256, 0, g.stream>>>(p);
         else if (c.f == 2) linear_tile<DT, AX, BX, OUT, 2, 2, false><<<blocks, 256, 0, g.stream>>>(p);
         else if constexpr (DT != kF32) linear_tile<DT, AX, BX, OUT, 4, 4, false><<<blocks, 256, 0, g.stream>>>(p);
     }
