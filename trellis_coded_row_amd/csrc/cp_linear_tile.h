@@ -286,9 +286,9 @@ __device__ __forceinline__ TilePlace place_of(const TileParams &p, uint32_t BM, 
 // A step of 4 x 4 fragments reads 8 of them for 16 products, which LDS hides
 // behind the products; its accumulators leave one wave for each SIMD, so the
 // next fragments are read between the products of the present ones. 4,096 x
-// 4,096 x 24,576 in bf16: cp_linear 571 to 605 us (1.36 to 1.44 PFLOP/s; the
-// vendor library's product 542 to 628), cp_linear_dx 640 to 652 (618 to 722),
-// cp_linear_dw 665 to 677 (709 to 824 for a 16-bit output). Its matrix units
+// 4,096 x 24,576 in bf16: cp_linear 571 to 610 us (1.35 to 1.44 PFLOP/s; the
+// vendor library's product 542 to 628), cp_linear_dx 640 to 659 (618 to 722),
+// cp_linear_dw 665 to 678 (709 to 824 for a 16-bit output). Its matrix units
 // are busy 83% of the cycles (71 and 68% where operands are read across, at two LDS
 // reads a fragment), at a clock that gives way to the power they draw: with
 // zeros for operands the same launches take 458, 498 and 495 us.
