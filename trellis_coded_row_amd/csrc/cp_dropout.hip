@@ -27,6 +27,7 @@ struct Layout {
 // gradient, which needs the registers.
 constexpr uint32_t kDropRows = 4, kGradRows = 2;
 
+// (n is not 0)
 Layout layout_of(uint64_t m, uint64_t n, int dtype, uint32_t rows)
 {
     constexpr uint64_t most = 2048;  // workgroups: eight for each compute unit

@@ -129,7 +129,7 @@ cp_status cp_linear(const void *x, uint64_t x_stride, const void *w, uint64_t w_
 
 uint64_t cp_linear_act_grad_workspace_bytes(uint64_t m, uint64_t n)
 {
-    if (m > kMaxCount || n > kMaxCount) return 0;
+    if (n == 0 || m > kMaxCount || n > kMaxCount) return 0;
     return cpk::act_grad_workspace_bytes(m, n);
 }
 
