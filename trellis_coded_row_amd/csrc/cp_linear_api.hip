@@ -143,19 +143,21 @@ cp_status cp_linear_act_grad(const void *dy, uint64_t dy_stride, const void *z, 
     const uint64_t es = cpk::dtype_bytes(dtype);
     if (!good_or_null(db, 4)) return CP_ERR_INVALID_ARGUMENT;
     if (n == 0) return CP_OK;
+    // (without rows db becomes zeros, by the same launches)
+    const Range sums = range_of(db, 1, n, n, 4), numbers = range_of(a.drop.rng, 1, 2, 2, 8);
+    if (db && !workspace_ok(workspace, workspace_bytes, cpk::act_grad_workspace_bytes(m, n)))
+        return CP_ERR_INVALID_ARGUMENT;
+    if (overlap(sums, numbers)) return CP_ERR_INVALID_ARGUMENT;
     if (m > 0) {
         if (!good(dy, es) || !good(dz, es)) return CP_ERR_INVALID_ARGUMENT;
         if (act != CP_ACT_NONE && (!good(z, es) || !spans(m, z_stride))) return CP_ERR_INVALID_ARGUMENT;
-        if (db && !workspace_ok(workspace, workspace_bytes, cpk::act_grad_workspace_bytes(m, n)))
-            return CP_ERR_INVALID_ARGUMENT;
-        const Range out = range_of(dz, m, n, n, es), sums = range_of(db, 1, n, n, 4);
-        const Range numbers = range_of(a.drop.rng, 1, 2, 2, 8);
+        const Range out = range_of(dz, m, n, n, es);
         const Range in[2] = {range_of(dy, m, n, dy_stride, es),
                              range_of(act == CP_ACT_NONE ? nullptr : z, m, n, z_stride, es)};
         const bool itself[2] = {dy == dz && (m == 1 || dy_stride == n), z == dz && (m == 1 || z_stride == n)};
         for (int q = 0; q < 2; ++q)
             if (overlap(sums, in[q]) || (!itself[q] && overlap(out, in[q]))) return CP_ERR_INVALID_ARGUMENT;
-        if (overlap(out, sums) || overlap(out, numbers) || overlap(sums, numbers)) return CP_ERR_INVALID_ARGUMENT;
+        if (overlap(out, sums) || overlap(out, numbers)) return CP_ERR_INVALID_ARGUMENT;
     }
     if (m == 0 && !db) return CP_OK;
     forget_earlier_error();
