@@ -174,9 +174,11 @@ struct Slopes {
     static __device__ __forceinline__ float at(const f32x4 *cubic, float z)
     {
         if constexpr (!TABLE) return act_slope<ACT>(z);
-        // (a minimum that keeps NaN; it then falls to point 0 with a NaN on the way to the next)
-        const float u = __builtin_elementwise_minimum(kPoints * __builtin_fabsf(z), 511.99997f);
-        const f32x4 c = cubic[(uint32_t)u];
+        // NaN takes the last point's place (a whole number cannot be made of it) and stays NaN on the way to the next
+        const float far = kPoints * __builtin_fabsf(z), last = 511.99997f;
+        const uint32_t point = (uint32_t)__builtin_fminf(far, last);
+        const float u = __builtin_elementwise_minimum(far, last);
+        const f32x4 c = cubic[point];
         const float f = __builtin_amdgcn_fractf(u);
         const float odd = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(c[3], f, c[2]), f, c[1]), f, c[0]);
         return 0.5f + __builtin_copysignf(odd, z);
