@@ -133,55 +133,71 @@ __global__ __launch_bounds__(256) void dropout_rows(const typename Elem<DT>::raw
     else if (p.c < d) rows(std::false_type{});
 }
 
-// The slope of an activation as cubics between 512 points from 0 up, 1 / kPoints
-// apart, in LDS: act'(-z) = 1 - act'(z) for the smooth ones, so that the odd
-// part act' - 1/2 is held for z >= 0. Hermite's cubics through the slope and its
-// derivative are off by 5e-9 (gelu), 3e-8 (silu) and 1e-8 (gelu_tanh) at most,
-// and past the last point the slope is 1 in 32 bits. A slope then takes ten
-// vector instructions and one read, where the formula takes up to 30 and
-// bounded the time: 8,192 x 16,384 in bf16 with gelu and dropout 150 us (5.4
-// TB/s), by the formula 276.
+// The slope of a smooth activation from 512 cubics in LDS, for |z| in pieces of
+// 1 / PIECES: of the slope at -|z|, from which that at |z| is 1 less it, so that
+// a slope far below 0 keeps its own size's precision (held as 1/2 and an odd
+// part it would be the difference of two halves, off by 3e-8 whatever its size).
+// A piece's cubic goes through the slope at its ends and a quarter from each, and
+// is off by at most h^4 / 1536 times the fourth derivative: 5 x 2^-24 of the
+// slope's terms where it falls fastest. With the roundings of the four values
+// and of the cubic's own a slope is within 44 x 2^-24 of them (7 at most in 2^21
+// values of each). From -DEEP down the formula takes over, for values of a wave
+// that has some; past DEEP the slope is 1.
+// The formula alone would bound the time: 8,192 x 16,384 in bf16 with dropout and
+// z of deviation 1.5 takes 152 to 154 us with gelu (5.3 TB/s; by the formula
+// 169), 152 with gelu_tanh (181), 151 with silu (154). With z of deviation 6, where
+// every wave has deep values, 181, 192 and 154.
 template <int ACT>
 struct Slopes {
-    static constexpr float kPoints = ACT == kSilu ? 16.0f : 32.0f;
     static constexpr bool TABLE = ACT == kGelu || ACT == kGeluTanh || ACT == kSilu;
     static constexpr uint32_t COUNT = TABLE ? 512 : 1;
-
-    // the slope's derivative
-    static __device__ __forceinline__ float derivative(float z)
-    {
-        if constexpr (ACT == kGelu) return 0.3989422804014327f * exp_of(-0.5f * z * z) * (2.0f - z * z);
-        const float u = ACT == kSilu ? z : 1.5957691216057308f * (z + 0.044715f * z * z * z);
-        const float w = ACT == kSilu ? 1.0f : 1.5957691216057308f * (1.0f + 0.134145f * z * z);
-        const float bend = ACT == kSilu ? 0.0f : 1.5957691216057308f * 0.26829f * z;
-        const float g = reciprocal(1.0f + exp_of(-u));
-        return g * (1.0f - g) * (2.0f * w + z * ((1.0f - 2.0f * g) * w * w + bend));
-    }
+    static constexpr float PIECES = ACT == kSilu ? 16.0f : 64.0f;  // for each 1 of |z|
+    static constexpr float DEEP = ACT == kSilu ? 32.0f : ACT == kGelu ? 8.0f : 6.0f;  // (a gelu_tanh falls faster)
 
     static __device__ __forceinline__ void fill(f32x4 *cubic)
     {
         if constexpr (TABLE) {
             for (uint32_t i = threadIdx.x; i < COUNT; i += 256) {
-                const float z0 = (float)i / kPoints, z1 = (float)(i + 1) / kPoints;
-                const float p0 = act_slope<ACT>(z0) - 0.5f, p1 = act_slope<ACT>(z1) - 0.5f;
-                const float m0 = derivative(z0) / kPoints, m1 = derivative(z1) / kPoints;
-                cubic[i] = f32x4{p0, m0, 3.0f * (p1 - p0) - 2.0f * m0 - m1, 2.0f * (p0 - p1) + m0 + m1};
+                const auto slope = [&](float at) { return act_slope_below<ACT>(((float)i + at) * (1.0f / PIECES)); };
+                const float a0 = slope(0.0f), b0 = slope(0.25f), b1 = slope(0.75f), a1 = slope(1.0f);
+                const float even_a = 0.5f * (a1 + a0), odd_a = a1 - a0, even_b = 0.5f * (b1 + b0), odd_b = 2.0f * (b1 - b0);
+                // about the middle, then from the piece's start
+                const float c2 = (even_a - even_b) * (16.0f / 3.0f), c3 = (odd_a - odd_b) * (16.0f / 3.0f);
+                const float c1 = odd_b - 0.0625f * c3;
+                cubic[i] = f32x4{a0, c1 - c2 + 0.75f * c3, c2 - 1.5f * c3, c3};
             }
             __syncthreads();
         }
     }
 
+    // of z above -DEEP
     static __device__ __forceinline__ float at(const f32x4 *cubic, float z)
     {
         if constexpr (!TABLE) return act_slope<ACT>(z);
-        // NaN takes the last point's place (a whole number cannot be made of it) and stays NaN on the way to the next
-        const float far = kPoints * __builtin_fabsf(z), last = 511.99997f;
-        const uint32_t point = (uint32_t)__builtin_fminf(far, last);
-        const float u = __builtin_elementwise_minimum(far, last);
-        const f32x4 c = cubic[point];
-        const float f = __builtin_amdgcn_fractf(u);
-        const float odd = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(c[3], f, c[2]), f, c[1]), f, c[0]);
-        return 0.5f + __builtin_copysignf(odd, z);
+        // NaN takes the last piece (a whole number cannot be made of it) and stays NaN on the way through it
+        const float far = PIECES * __builtin_fabsf(z), last = 511.99997f;
+        const f32x4 c = cubic[(uint32_t)__builtin_fminf(far, last)];
+        const float f = __builtin_amdgcn_fractf(__builtin_elementwise_minimum(far, last));
+        const float below = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(c[3], f, c[2]), f, c[1]), f, c[0]);
+        return z < 0.0f ? below : 1.0f - below;
+    }
+
+    // The slopes at 8 values.
+    static __device__ __forceinline__ void at8(const f32x4 *cubic, const float *z, float *slope)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) slope[e] = at(cubic, z[e]);
+        if constexpr (TABLE) {
+            // the largest bits are those of the value furthest below 0 (or of a NaN)
+            uint32_t low = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) low = __float_as_uint(z[e]) > low ? __float_as_uint(z[e]) : low;
+            if (low >= __float_as_uint(-DEEP)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (z[e] <= -DEEP) slope[e] = act_slope<ACT>(z[e]);
+            }
+        }
     }
 };
 
@@ -212,9 +228,14 @@ __global__ __launch_bounds__(256) void act_grad_rows(const typename Elem<DT>::ra
             [&](uint32_t q, uint64_t row) {
                 float f[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    f[e] = Elem<DT>::get(v[q][e]);
-                    if constexpr (ACT != kNone) f[e] *= S::at(lds.cubic, Elem<DT>::get(s[q][e]));
+                for (int e = 0; e < 8; ++e) f[e] = Elem<DT>::get(v[q][e]);
+                if constexpr (ACT != kNone) {
+                    float z8[8], slope[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z8[e] = Elem<DT>::get(s[q][e]);
+                    S::at8(lds.cubic, z8, slope);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] *= slope[e];
                 }
                 if (mask.threshold) drop8(mask, (uint32_t)row, p.c, f);
 #pragma unroll

@@ -135,21 +135,17 @@ __device__ __forceinline__ void drop8(const Mask &m, uint32_t row, uint32_t c, f
 // infinity times the 0 it meets would give NaN.
 __device__ __forceinline__ float from_below(float z) { return z < -1e4f ? -1e4f : z; }
 
-__device__ __forceinline__ float within(float z) { return z < -1e4f ? -1e4f : z > 1e4f ? 1e4f : z; }
-
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(1.4426950408889634f * x); }
 
 __device__ __forceinline__ float reciprocal(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// Phi(z) of the normal distribution and exp(-z^2 / 2). Phi(-x) exp(x^2 / 2) is
-// smooth in t = 1 / (1 + 0.35 x) for x >= 0 and goes to 0 with it: t times a
-// polynomial of degree 8, fitted here over x < 14 (beyond, the exponential
-// is 0) to the least relative error, 3.2e-8. In 32 bits z Phi(z) is then within
-// 1.2 x 2^-24 (1 + |z|), and the slope within 3 x 2^-24, at a fifth of the
-// library function's time.
-__device__ __forceinline__ float normal_share(float z, float *exponential)
+// Phi(-x) exp(x^2 / 2) of the normal distribution. It is smooth in t = 1 / (1 +
+// 0.35 x) for x >= 0 and goes to 0 with it: t times a polynomial of degree 8,
+// fitted here over x < 14 (beyond, the exponential is 0) to the least relative
+// error, 3.2e-8.
+__device__ __forceinline__ float normal_tail(float x)
 {
-    const float t = reciprocal(__builtin_fmaf(0.35f, __builtin_fabsf(z), 1.0f));
+    const float t = reciprocal(__builtin_fmaf(0.35f, x, 1.0f));
     float p = -0.029145967215299606f;
     p = __builtin_fmaf(p, t, 0.14397187530994415f);
     p = __builtin_fmaf(p, t, -0.2557145953178406f);
@@ -159,8 +155,14 @@ __device__ __forceinline__ float normal_share(float z, float *exponential)
     p = __builtin_fmaf(p, t, 0.119832843542099f);
     p = __builtin_fmaf(p, t, 0.13986186683177948f);
     p = __builtin_fmaf(p, t, 0.13962140679359436f);
-    *exponential = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
-    const float tail = p * t * *exponential;
+    return p * t;
+}
+
+// Phi(z). In 32 bits z Phi(z) is then within 1.2 x 2^-24 (1 + |z|), at a fifth
+// of the library function's time.
+__device__ __forceinline__ float normal_share(float z)
+{
+    const float tail = normal_tail(__builtin_fabsf(z)) * __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
     return z < 0.0f ? tail : 1.0f - tail;
 }
 
@@ -169,9 +171,8 @@ __device__ __forceinline__ float act_value(float z)
 {
     if constexpr (ACT == kRelu) return z < 0.0f ? 0.0f : z;
     if constexpr (ACT == kGelu) {
-        float e;
         z = from_below(z);
-        return z * normal_share(z, &e);
+        return z * normal_share(z);
     }
     if constexpr (ACT == kGeluTanh) {
         z = from_below(z);
@@ -184,23 +185,68 @@ __device__ __forceinline__ float act_value(float z)
     return z;
 }
 
+// 2^(y + rest) for a y of up to 150 and its rounding's rest: an exponent in
+// one 32-bit number would carry that rounding, 10^-6 of the power's size.
+__device__ __forceinline__ float power_of_two(float y, float rest)
+{
+    const float e = __builtin_amdgcn_exp2f(y);
+    return __builtin_fmaf(0.6931471805599453f * e, rest, e);
+}
+
+// exp(-x), exp(-x^2 / 2) and exp(-2 u) of gelu_tanh's u = sqrt(2 / pi) (x +
+// 0.044715 x^3), for x of 0 to 10^4, within 4 x 2^-24 of their size (0 where
+// they are below 2^-126). Constants of the exponents come in two parts, and each
+// product with its rest.
+__device__ __forceinline__ float exp_minus(float x)
+{
+#pragma clang fp contract(off)
+    const float y = -1.4426950408889634f * x;
+    return power_of_two(y, __builtin_fmaf(-1.925963033e-8f, x, __builtin_fmaf(-1.4426950408889634f, x, -y)));
+}
+
+__device__ __forceinline__ float bell(float x)
+{
+#pragma clang fp contract(off)
+    const float h = x * x, l = __builtin_fmaf(x, x, -h), y = -0.72134752044448170f * h;
+    const float rest = __builtin_fmaf(-0.72134752044448170f, l, __builtin_fmaf(-0.72134752044448170f, h, -y));
+    return power_of_two(y, __builtin_fmaf(-9.629815167e-9f, h, rest));
+}
+
+__device__ __forceinline__ float exp_minus_cubic(float x)
+{
+#pragma clang fp contract(off)
+    // x (2.302 + 0.1029 x^2), the factors of x with 2 sqrt(2 / pi) / log(2)
+    const float a = 2.302208185195923f, b = 0.10294324159622192f;
+    const float h = x * x, l = __builtin_fmaf(x, x, -h), w = b * h;
+    const float w_rest = __builtin_fmaf(-2.0161985415e-9f, h, __builtin_fmaf(b, l, __builtin_fmaf(b, h, -w)));
+    const float s = a + w, of_w = s - a;  // (a sum and its rounding, whichever is larger)
+    const float s_rest = ((a - (s - of_w)) + (w - of_w)) + w_rest + 1.2948402350e-8f;
+    const float y = -s * x;
+    return power_of_two(y, __builtin_fmaf(-s_rest, x, __builtin_fmaf(-s, x, -y)));
+}
+
+// The slope at -x of a smooth activation, for x of 0 to 10^4; at x it is 1 less
+// that. Near 0 for a large x, and then to its own size: a product of the
+// exponential and what is left of the slope's two terms, within 16 x 2^-24 of
+// their magnitudes.
+template <int ACT>
+__device__ __forceinline__ float act_slope_below(float x)
+{
+    static_assert(ACT == kGelu || ACT == kGeluTanh || ACT == kSilu, "");
+    if constexpr (ACT == kGelu)
+        return bell(x) * __builtin_fmaf(-0.3989422804014327f, x, normal_tail(x));
+    const float e = ACT == kSilu ? exp_minus(x) : exp_minus_cubic(x), r = reciprocal(1.0f + e);
+    const float bend = ACT == kSilu ? 1.0f : 1.5957691216057308f * __builtin_fmaf(0.134145f, x * x, 1.0f);
+    return e * r * __builtin_fmaf(-x * r, bend, 1.0f);
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z)
 {
     if constexpr (ACT == kRelu) return z > 0.0f ? 1.0f : 0.0f;
-    z = within(z);
-    if constexpr (ACT == kGelu) {
-        float e;
-        const float share = normal_share(z, &e);
-        return __builtin_fmaf(0.3989422804014327f * z, e, share);
-    }
-    if constexpr (ACT == kGeluTanh) {
-        const float g = reciprocal(1.0f + exp_of(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-        return g + z * g * (1.0f - g) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
-    }
-    if constexpr (ACT == kSilu) {
-        const float g = reciprocal(1.0f + exp_of(-z));
-        return g + z * g * (1.0f - g);
+    if constexpr (ACT == kGelu || ACT == kGeluTanh || ACT == kSilu) {
+        const float below = act_slope_below<ACT>(__builtin_elementwise_minimum(__builtin_fabsf(z), 1e4f));
+        return z < 0.0f ? below : 1.0f - below;
     }
     return 1.0f;
 }
