@@ -26,9 +26,10 @@
  *   relu max(z, 0) (slope 0 at 0), gelu z Phi(z), Phi the normal distribution,
  *   gelu_tanh z / (1 + exp(-2 u)) with u = sqrt(2 / pi) (z + 0.044715 z^3),
  *   silu z / (1 + exp(-z)).
- * Each but relu is z share(z), its slope share + z share'. The slope is within
- * 48 x 2^-24 of these two terms' magnitudes, so it keeps its precision however
- * far below 0 z lies; an exponential below 2^-126 may count as 0. At NaN relu's
+ * Each but relu is z share(z), its slope share + z share'. However far below 0 z
+ * lies, the value is within 18 x 2^-24 of its size (2^-15 of it for a dtype of 16
+ * bits) and the slope within 48 x 2^-24 of its two terms' magnitudes, before
+ * they are rounded; an exponential below 2^-126 may count as 0. At NaN relu's
  * slope is 0, the others' NaN.
  *
  * Conventions as in cp_ops.h: types, statuses, strides in elements, inputs

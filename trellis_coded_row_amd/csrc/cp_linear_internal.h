@@ -131,12 +131,6 @@ __device__ __forceinline__ void drop8(const Mask &m, uint32_t row, uint32_t c, f
     }
 }
 
-// z kept where its functions are at their limits anyway, NaN as it is: an
-// infinity times the 0 it meets would give NaN.
-__device__ __forceinline__ float from_below(float z) { return z < -1e4f ? -1e4f : z; }
-
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(1.4426950408889634f * x); }
-
 __device__ __forceinline__ float reciprocal(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // Phi(-x) exp(x^2 / 2) of the normal distribution. It is smooth in t = 1 / (1 +
@@ -158,33 +152,6 @@ __device__ __forceinline__ float normal_tail(float x)
     return p * t;
 }
 
-// Phi(z). In 32 bits z Phi(z) is then within 1.2 x 2^-24 (1 + |z|), at a fifth
-// of the library function's time.
-__device__ __forceinline__ float normal_share(float z)
-{
-    const float tail = normal_tail(__builtin_fabsf(z)) * __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
-    return z < 0.0f ? tail : 1.0f - tail;
-}
-
-template <int ACT>
-__device__ __forceinline__ float act_value(float z)
-{
-    if constexpr (ACT == kRelu) return z < 0.0f ? 0.0f : z;
-    if constexpr (ACT == kGelu) {
-        z = from_below(z);
-        return z * normal_share(z);
-    }
-    if constexpr (ACT == kGeluTanh) {
-        z = from_below(z);
-        return z * reciprocal(1.0f + exp_of(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-    }
-    if constexpr (ACT == kSilu) {
-        z = from_below(z);
-        return z * reciprocal(1.0f + exp_of(-z));
-    }
-    return z;
-}
-
 // 2^(y + rest) for a y of up to 150 and its rounding's rest: an exponent in
 // one 32-bit number would carry that rounding, 10^-6 of the power's size.
 __device__ __forceinline__ float power_of_two(float y, float rest)
@@ -194,35 +161,74 @@ __device__ __forceinline__ float power_of_two(float y, float rest)
 }
 
 // exp(-x), exp(-x^2 / 2) and exp(-2 u) of gelu_tanh's u = sqrt(2 / pi) (x +
-// 0.044715 x^3), for x of 0 to 10^4, within 4 x 2^-24 of their size (0 where
-// they are below 2^-126). Constants of the exponents come in two parts, and each
-// product with its rest.
+// 0.044715 x^3) (0 where they are below 2^-126). WIDE, for what stays in 32 bits
+// and x of 0 to 10^4: within 4 x 2^-24 of their size, the exponents' constants in
+// two parts, and each product with its rest. Else the exponent is one 32-bit
+// number, off by up to 343 x 2^-24 of the power's size (2^-15.6), which a result
+// of 16 bits does not show, and x may be below 0.
+template <bool WIDE>
 __device__ __forceinline__ float exp_minus(float x)
 {
 #pragma clang fp contract(off)
     const float y = -1.4426950408889634f * x;
+    if constexpr (!WIDE) return __builtin_amdgcn_exp2f(y);
     return power_of_two(y, __builtin_fmaf(-1.925963033e-8f, x, __builtin_fmaf(-1.4426950408889634f, x, -y)));
 }
 
+template <bool WIDE>
 __device__ __forceinline__ float bell(float x)
 {
 #pragma clang fp contract(off)
-    const float h = x * x, l = __builtin_fmaf(x, x, -h), y = -0.72134752044448170f * h;
+    const float h = x * x, y = -0.72134752044448170f * h;
+    if constexpr (!WIDE) return __builtin_amdgcn_exp2f(y);
+    const float l = __builtin_fmaf(x, x, -h);
     const float rest = __builtin_fmaf(-0.72134752044448170f, l, __builtin_fmaf(-0.72134752044448170f, h, -y));
     return power_of_two(y, __builtin_fmaf(-9.629815167e-9f, h, rest));
 }
 
+template <bool WIDE>
 __device__ __forceinline__ float exp_minus_cubic(float x)
 {
 #pragma clang fp contract(off)
     // x (2.302 + 0.1029 x^2), the factors of x with 2 sqrt(2 / pi) / log(2)
-    const float a = 2.302208185195923f, b = 0.10294324159622192f;
-    const float h = x * x, l = __builtin_fmaf(x, x, -h), w = b * h;
+    const float a = 2.302208185195923f, b = 0.10294324159622192f, h = x * x;
+    if constexpr (!WIDE) return __builtin_amdgcn_exp2f(-x * __builtin_fmaf(b, h, a));
+    const float l = __builtin_fmaf(x, x, -h), w = b * h;
     const float w_rest = __builtin_fmaf(-2.0161985415e-9f, h, __builtin_fmaf(b, l, __builtin_fmaf(b, h, -w)));
     const float s = a + w, of_w = s - a;  // (a sum and its rounding, whichever is larger)
     const float s_rest = ((a - (s - of_w)) + (w - of_w)) + w_rest + 1.2948402350e-8f;
     const float y = -s * x;
     return power_of_two(y, __builtin_fmaf(-s_rest, x, __builtin_fmaf(-s, x, -y)));
+}
+
+// An activation by its share, z share(z) with share(-z) = 1 - share(z). Below 0
+// the share goes to 0, and is computed to its own size: a value is within 18 x
+// 2^-24 of its size where WIDE, else within 2^-15 (1,000 x 2,050 x 1,030 in f16 with
+// gelu_tanh takes 19.0 us, and 20.9 where WIDE). Past 10^4 the share is at its
+// limit anyway, and an infinity would meet the 0 it goes to.
+template <int ACT, bool WIDE>
+__device__ __forceinline__ float act_value(float z)
+{
+    if constexpr (ACT == kRelu) return z < 0.0f ? 0.0f : z;
+    if constexpr (ACT == kGelu || ACT == kGeluTanh || ACT == kSilu) {
+        const float from = __builtin_elementwise_maximum(z, -1e4f);  // (NaN stays)
+        if constexpr (ACT != kGelu && !WIDE) {
+            const float e = ACT == kSilu ? exp_minus<false>(from) : exp_minus_cubic<false>(from);
+            return from * reciprocal(1.0f + e);
+        }
+        const float x = __builtin_elementwise_minimum(__builtin_fabsf(z), 1e4f);
+        float below, above;
+        if constexpr (ACT == kGelu) {
+            below = bell<WIDE>(x) * normal_tail(x);
+            above = 1.0f - below;
+        } else {
+            const float e = ACT == kSilu ? exp_minus<WIDE>(x) : exp_minus_cubic<WIDE>(x);
+            above = reciprocal(1.0f + e);
+            below = e * above;
+        }
+        return from * (z < 0.0f ? below : above);
+    }
+    return z;
 }
 
 // The slope at -x of a smooth activation, for x of 0 to 10^4; at x it is 1 less
@@ -234,8 +240,8 @@ __device__ __forceinline__ float act_slope_below(float x)
 {
     static_assert(ACT == kGelu || ACT == kGeluTanh || ACT == kSilu, "");
     if constexpr (ACT == kGelu)
-        return bell(x) * __builtin_fmaf(-0.3989422804014327f, x, normal_tail(x));
-    const float e = ACT == kSilu ? exp_minus(x) : exp_minus_cubic(x), r = reciprocal(1.0f + e);
+        return bell<true>(x) * __builtin_fmaf(-0.3989422804014327f, x, normal_tail(x));
+    const float e = ACT == kSilu ? exp_minus<true>(x) : exp_minus_cubic<true>(x), r = reciprocal(1.0f + e);
     const float bend = ACT == kSilu ? 1.0f : 1.5957691216057308f * __builtin_fmaf(0.134145f, x * x, 1.0f);
     return e * r * __builtin_fmaf(-x * r, bend, 1.0f);
 }
@@ -251,11 +257,11 @@ __device__ __forceinline__ float act_slope(float z)
     return 1.0f;
 }
 
-template <int ACT>
+template <int ACT, bool WIDE>
 __device__ __forceinline__ void act_values(float *f)
 {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = act_value<ACT>(f[e]);
+    for (int e = 0; e < 8; ++e) f[e] = act_value<ACT, WIDE>(f[e]);
 }
 
 // The bias of columns [c, c + 8), zeros without one.
@@ -288,10 +294,11 @@ __device__ __forceinline__ void finish8(const Epilogue &e, const Mask &mask, uin
         for (int q = 0; q < 8; ++q) f[q] += bias[q];
     }
     if (e.z) store8<OUT>((typename Elem<OUT>::raw *)e.z + row * n, c, n, f);
-    if (e.act == kRelu) act_values<kRelu>(f);
-    else if (e.act == kGelu) act_values<kGelu>(f);
-    else if (e.act == kGeluTanh) act_values<kGeluTanh>(f);
-    else if (e.act == kSilu) act_values<kSilu>(f);
+    constexpr bool WIDE = OUT == kF32;
+    if (e.act == kRelu) act_values<kRelu, WIDE>(f);
+    else if (e.act == kGelu) act_values<kGelu, WIDE>(f);
+    else if (e.act == kGeluTanh) act_values<kGeluTanh, WIDE>(f);
+    else if (e.act == kSilu) act_values<kSilu, WIDE>(f);
     if (mask.threshold) drop8(mask, (uint32_t)row, c, f);
     if (e.residual) {
 #pragma unroll
