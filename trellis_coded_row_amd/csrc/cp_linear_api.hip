@@ -27,7 +27,7 @@ static bool good_or_null(const void *p, uint64_t bytes) { return ((uintptr_t)p &
 // Byte ranges of n rows, `stride` elements apart, stay below 2^62.
 static bool spans(uint64_t n, uint64_t stride) { return n == 0 || stride <= (1ull << 60) / n; }
 
-// The bytes of n rows of d elements, `stride` apart.
+// The bytes of n rows of d elements, `stride` apart; nowhere without values.
 struct Range {
     uintptr_t begin, end;
 };
@@ -35,7 +35,7 @@ struct Range {
 static Range range_of(const void *p, uint64_t n, uint64_t d, uint64_t stride, uint64_t es)
 {
     const uintptr_t at = (uintptr_t)p;
-    if (!p || n == 0 || d == 0) return {at, at};
+    if (!p || n == 0 || d == 0) return {0, 0};
     return {at, at + ((n - 1) * stride + d) * es};
 }
 
