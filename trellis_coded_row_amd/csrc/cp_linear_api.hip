@@ -30,16 +30,27 @@ static bool spans(uint64_t n, uint64_t stride) { return n == 0 || stride <= (1ul
 // The bytes of n rows of d elements, `stride` apart; nowhere without values.
 struct Range {
     uintptr_t begin, end;
+    uint64_t row, pitch;  // bytes of a row, and from one to the next (0: a single one)
 };
 
 static Range range_of(const void *p, uint64_t n, uint64_t d, uint64_t stride, uint64_t es)
 {
     const uintptr_t at = (uintptr_t)p;
-    if (!p || n == 0 || d == 0) return {0, 0};
-    return {at, at + ((n - 1) * stride + d) * es};
+    if (!p || n == 0 || d == 0) return {0, 0, 0, 0};
+    return {at, at + ((n - 1) * stride + d) * es, d * es, n > 1 ? stride * es : 0};
 }
 
-static bool overlap(Range a, Range b) { return a.begin < b.end && b.begin < a.end; }
+// Whether a's rows and b's lie between each other all the way: rows equally far
+// apart, b's behind a's and before the next of them.
+static bool between(Range a, Range b)
+{
+    const uint64_t pitch = a.pitch ? a.pitch : b.pitch;
+    if (pitch == 0 || (b.pitch && b.pitch != pitch)) return false;
+    const uint64_t behind = b.begin >= a.begin ? (b.begin - a.begin) % pitch : (pitch - (a.begin - b.begin) % pitch) % pitch;
+    return behind >= a.row && behind + b.row <= pitch;
+}
+
+static bool overlap(Range a, Range b) { return a.begin < b.end && b.begin < a.end && !between(a, b); }
 
 // The mask's threshold from the share that is dropped, and whether that is one.
 static bool drop_of(double p, const uint64_t *rng, cpk::Drop *out)
