@@ -35,7 +35,8 @@
  * Conventions as in cp_ops.h: types, statuses, strides in elements, inputs
  * whose rows may overlap, 32-bit arithmetic with one rounding where a result
  * is stored, equal calls give equal bits. An output must not overlap an input
- * or another output, except where a call says so.
+ * or another output, except where a call says so; rows of one may lie between
+ * rows of another, equally far apart.
  */
 #ifndef CP_LINEAR_H
 #define CP_LINEAR_H
@@ -77,15 +78,17 @@ cp_status cp_linear(const void *x, uint64_t x_stride, const void *w, uint64_t w_
                     cp_act act, double p, const uint64_t *rng, void *y, uint64_t y_stride, void *z_out,
                     void *workspace, uint64_t workspace_bytes, void *stream);
 
-/* Device workspace bytes of cp_linear_act_grad with a db (0 without). */
+/* Device workspace bytes of cp_linear_act_grad with a db, also where m is 0 (0
+ * without one, and for n = 0). */
 uint64_t cp_linear_act_grad_workspace_bytes(uint64_t m, uint64_t n);
 
 /* Back through cp_linear's epilogue: dz = drop(dy) act'(z), db[j] = the sum of
- * dz over rows, in 32 bits from the unrounded dz (float[n], may be NULL). z is
- * what cp_linear stored (rounded: the slope is taken at slightly another point
- * than z); not read, and may be NULL, with CP_ACT_NONE. dy and z have dtype and
- * row strides of their own; dz is contiguous and may be dy, z or both
- * themselves, where those are contiguous. The gradient of the residual is dy.
+ * dz over rows, in 32 bits from the unrounded dz (float[n], may be NULL; zeros
+ * where m is 0). z is what cp_linear stored (rounded: the slope is taken at
+ * slightly another point than z); not read, and may be NULL, with CP_ACT_NONE.
+ * dy and z have dtype and row strides of their own; dz is contiguous and may be
+ * dy, z or both themselves, where those are contiguous. The gradient of the
+ * residual is dy.
  * Errors: INVALID_ARGUMENT, HIP. */
 cp_status cp_linear_act_grad(const void *dy, uint64_t dy_stride, const void *z, uint64_t z_stride, cp_dtype dtype,
                              uint64_t m, uint64_t n, cp_act act, double p, const uint64_t *rng, void *dz, float *db,
@@ -105,7 +108,7 @@ cp_status cp_linear_dx(const void *dz, uint64_t dz_stride, const void *w, uint64
                        void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* dw[j][l] = sum over i of dz[i][j] x[i][l], in 32 bits (float, n x k, rows
- * dw_stride apart); with add != 0 that is added to what dw holds. dz - m x n
+ * dw_stride apart). add - 0, or 1: that is added to what dw holds. dz - m x n
  * and x - m x k have dtype.
  * Errors: as cp_linear_dx. */
 cp_status cp_linear_dw(const void *dz, uint64_t dz_stride, const void *x, uint64_t x_stride, cp_dtype dtype,
